@@ -55,6 +55,13 @@ class moe_sizes_t(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in _SIZE_FIELDS]
 
 
+_EXPERT_SIZE_FIELDS = ["w1", "w1_scale", "w2", "w2_scale", "h", "h_scale"]
+
+
+class moe_expert_sizes_t(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in _EXPERT_SIZE_FIELDS]
+
+
 _vp = ctypes.c_void_p
 _SIGS = {
     "moe_sizes": [ctypes.POINTER(moe_shape), ctypes.POINTER(moe_sizes_t)],
@@ -70,6 +77,10 @@ _SIGS = {
     "moe_combine_acc_send": [ctypes.POINTER(moe_shape)] + [_vp] * 10,
     "moe_combine_acc_recv": [ctypes.POINTER(moe_shape)] + [_vp] * 5,
     "moe_expert_stub": [ctypes.POINTER(moe_shape), ctypes.c_int32] + [_vp] * 5,
+    "moe_expert_gemm": [ctypes.POINTER(moe_shape)] + [ctypes.c_int32] * 2 + [_vp] * 7,
+    "moe_expert_gated": [ctypes.POINTER(moe_shape)] + [ctypes.c_int32] * 2 + [_vp] * 8,
+    "moe_expert_sizes": [ctypes.POINTER(moe_shape), ctypes.c_int32, ctypes.POINTER(moe_expert_sizes_t)],
+    "moe_expert_mlp": [ctypes.POINTER(moe_shape), ctypes.c_int32] + [_vp] * 11,
     "moe_prefill_dispatch": [ctypes.POINTER(moe_shape)] + [_vp] * 11,
     "moe_prefill_combine_local": [ctypes.POINTER(moe_shape)] + [_vp] * 6,
     "moe_prefill_allreduce": [ctypes.POINTER(moe_shape)] + [_vp] * 3,
@@ -239,6 +250,32 @@ def moe_expert_stub(shape, mode, expert_x, expert_scale, expert_off, expert_y, s
         _ptr(expert_y), _stream(stream)))
 
 
+def moe_expert_gemm(shape, K, C, a, a_scale, w, w_scale, expert_off, y, stream=None):
+    _check("moe_expert_gemm", _lib.moe_expert_gemm(
+        ctypes.byref(shape), int(K), int(C), _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale),
+        _ptr(expert_off), _ptr(y), _stream(stream)))
+
+
+def moe_expert_gated(shape, K, I, a, a_scale, w, w_scale, expert_off, h, h_scale, stream=None):
+    _check("moe_expert_gated", _lib.moe_expert_gated(
+        ctypes.byref(shape), int(K), int(I), _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale),
+        _ptr(expert_off), _ptr(h), _ptr(h_scale), _stream(stream)))
+
+
+def moe_expert_sizes(shape: moe_shape, I) -> dict:
+    out = moe_expert_sizes_t()
+    _check("moe_expert_sizes", _lib.moe_expert_sizes(ctypes.byref(shape), int(I), ctypes.byref(out)))
+    return {f: int(getattr(out, f)) for f in _EXPERT_SIZE_FIELDS}
+
+
+def moe_expert_mlp(shape, I, expert_x, expert_scale, w1, w1_scale, w2, w2_scale, expert_off, h, h_scale,
+                   expert_y, stream=None):
+    _check("moe_expert_mlp", _lib.moe_expert_mlp(
+        ctypes.byref(shape), int(I), _ptr(expert_x), _ptr(expert_scale), _ptr(w1), _ptr(w1_scale),
+        _ptr(w2), _ptr(w2_scale), _ptr(expert_off), _ptr(h), _ptr(h_scale), _ptr(expert_y),
+        _stream(stream)))
+
+
 def moe_prefill_dispatch(shape, x, x_scale, topk_idx, slot_pos, expert_x, expert_scale,
                          expert_cnt, expert_off, expert_src, workspace, stream=None):
     _check("moe_prefill_dispatch", _lib.moe_prefill_dispatch(
@@ -364,6 +401,42 @@ def alloc_prefill_buffers(N, T, H, E, R, fp8=False, capacity=0, device="cuda",
     if with_status:
         shape.status = t["status"].data_ptr()
     return Buffers(shape, sz, t)
+
+
+@dataclass
+class Experts:
+    """The weights of every expert's MLP and the buffers of its intermediate rows, for one shape and
+    one intermediate size I (include/moe.h, moe_expert_mlp).  e4m3 arrays are uint8."""
+    I: int
+    w1: torch.Tensor
+    w1_scale: torch.Tensor | None
+    w2: torch.Tensor
+    w2_scale: torch.Tensor | None
+    h: torch.Tensor
+    h_scale: torch.Tensor | None
+
+
+def alloc_experts(b: Buffers, I) -> Experts:
+    """Allocate the weights and the intermediate rows for the buffers' shape (torch.empty; contents
+    undefined: the caller fills the weights)."""
+    sh = b.shape
+    moe_expert_sizes(sh, I)  # refuses what the kernels do not implement
+    N, E, H, B = sh.N, sh.E, sh.H, b.sizes["capacity"]
+    dev, fp8 = b.expert_x.device, sh.dtype != MOE_BF16
+    dt = torch.uint8 if fp8 else torch.int16
+
+    def scales(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=dev) if fp8 else None
+
+    return Experts(I, torch.empty((E, 2 * I, H), dtype=dt, device=dev), scales(E, 2 * I // 128, H // 128),
+                   torch.empty((E, H, I), dtype=dt, device=dev), scales(E, H // 128, I // 128),
+                   torch.empty((N, B, I), dtype=dt, device=dev), scales(N, B, I // 128))
+
+
+def run_experts(b: Buffers, x: Experts, stream=None):
+    """The experts' MLPs on the dispatched rows of either layout: expert_x -> expert_y."""
+    moe_expert_mlp(b.shape, x.I, b.expert_x, b.expert_scale, x.w1, x.w1_scale, x.w2, x.w2_scale,
+                   b.expert_off, x.h, x.h_scale, b.expert_y, stream)
 
 
 def run_prefill_dispatch(b: Buffers, bias=True, stream=None):

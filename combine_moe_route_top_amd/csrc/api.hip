@@ -36,6 +36,8 @@ hipError_t launch_prefill_local(const Dims&, const uint16_t*, const int32_t*, co
                                 float*, hipStream_t);
 hipError_t launch_prefill_allreduce(const Dims&, const float*, uint16_t*, hipStream_t);
 hipError_t launch_stream_copy(const void*, void*, long, hipStream_t);
+hipError_t launch_experts(const Dims&, bool, int, int, const void*, const float*, const void*, const float*,
+                          const int32_t*, void*, float*, hipStream_t);
 }  // namespace moe
 
 using moe::Dims;
@@ -426,6 +428,93 @@ int moe_prefill_combine(const moe_shape* shape, const uint16_t* expert_y, const 
                                               (hipStream_t)stream));
     if (rc) return rc;
     return hip_status(moe::launch_prefill_allreduce(D, partial, out, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ the experts' products
+
+// One product of K values a row and C columns (gated: C columns from 2C weight rows): sizes the
+// kernels implement.
+static int expert_widths(const Dims& D, bool gated, int K, int C) {
+    if (K < 1 || C < 1) return MOE_EINVAL;
+    if (K > (1 << 20) || C > (1 << 20)) return MOE_EUNSUPPORTED;
+    if (K % (D.fp8 ? 128 : 8) != 0) return MOE_EUNSUPPORTED;
+    if (C % (D.fp8 && gated ? 128 : 8) != 0) return MOE_EUNSUPPORTED;
+    return MOE_OK;
+}
+
+// A scale array is there for e4m3 operands and only for them.
+static bool scale_fits(const Dims& D, const float* s) { return D.fp8 ? aligned(s, 4) : !s; }
+
+extern "C" {
+
+int moe_expert_gemm(const moe_shape* shape, int32_t K, int32_t C, const void* a, const float* a_scale,
+                    const void* w, const float* w_scale, const int32_t* expert_off, uint16_t* y,
+                    void* stream) {
+    Dims D;
+    int rc = make_dims(shape, &D);
+    if (rc) return rc;
+    rc = expert_widths(D, false, K, C);
+    if (rc) return rc;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(expert_off, 4) || !aligned(y, 16)) return MOE_EINVAL;
+    if (!scale_fits(D, a_scale) || !scale_fits(D, w_scale)) return MOE_EINVAL;
+    return hip_status(moe::launch_experts(D, false, K, C, a, a_scale, w, w_scale, expert_off, y, nullptr,
+                                          (hipStream_t)stream));
+}
+
+int moe_expert_gated(const moe_shape* shape, int32_t K, int32_t I, const void* a, const float* a_scale,
+                     const void* w, const float* w_scale, const int32_t* expert_off, void* h,
+                     float* h_scale, void* stream) {
+    Dims D;
+    int rc = make_dims(shape, &D);
+    if (rc) return rc;
+    rc = expert_widths(D, true, K, I);
+    if (rc) return rc;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(expert_off, 4) || !aligned(h, 16)) return MOE_EINVAL;
+    if (!scale_fits(D, a_scale) || !scale_fits(D, w_scale) || !scale_fits(D, h_scale)) return MOE_EINVAL;
+    return hip_status(moe::launch_experts(D, true, K, I, a, a_scale, w, w_scale, expert_off, h, h_scale,
+                                          (hipStream_t)stream));
+}
+
+int moe_expert_sizes(const moe_shape* shape, int32_t I, moe_expert_sizes_t* out) {
+    Dims D;
+    int rc = make_dims(shape, &D);
+    if (rc) return rc;
+    rc = expert_widths(D, true, D.H, I);
+    if (rc) return rc;
+    if (!out) return MOE_EINVAL;
+    const int64_t E = D.E, H = D.H, rows = (int64_t)D.N * D.B, b = D.fp8 ? 1 : 2;
+    out->w1 = E * 2 * I * H * b;
+    out->w2 = E * H * I * b;
+    out->h = rows * I * b;
+    out->w1_scale = D.fp8 ? E * (2 * I / 128) * (H / 128) * 4 : 0;
+    out->w2_scale = D.fp8 ? E * (H / 128) * (I / 128) * 4 : 0;
+    out->h_scale = D.fp8 ? rows * (I / 128) * 4 : 0;
+    return MOE_OK;
+}
+
+int moe_expert_mlp(const moe_shape* shape, int32_t I, const void* expert_x, const float* expert_scale,
+                   const void* w1, const float* w1_scale, const void* w2, const float* w2_scale,
+                   const int32_t* expert_off, void* h, float* h_scale, uint16_t* expert_y,
+                   void* stream) {
+    Dims D;
+    int rc = make_dims(shape, &D);
+    if (rc) return rc;
+    rc = expert_widths(D, true, D.H, I);
+    if (rc) return rc;
+    // validate both products before launching either
+    if (!aligned(expert_x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(expert_off, 4) ||
+        !aligned(h, 16) || !aligned(expert_y, 16))
+        return MOE_EINVAL;
+    if (!scale_fits(D, expert_scale) || !scale_fits(D, w1_scale) || !scale_fits(D, w2_scale) ||
+        !scale_fits(D, h_scale))
+        return MOE_EINVAL;
+    rc = hip_status(moe::launch_experts(D, true, D.H, I, expert_x, expert_scale, w1, w1_scale, expert_off, h,
+                                        h_scale, (hipStream_t)stream));
+    if (rc) return rc;
+    return hip_status(moe::launch_experts(D, false, I, D.H, h, h_scale, w2, w2_scale, expert_off, expert_y,
+                                          nullptr, (hipStream_t)stream));
 }
 
 }  // extern "C"

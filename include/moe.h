@@ -21,7 +21,8 @@
  *    which also returns (and clears) an error an earlier HIP call on the same thread left unread;
  *    such an error is reported as MOE_EHIP by the next call.
  *  - Payload buffers (x, x_scale, send_buf, recv_buf, expert_x, expert_scale, expert_y,
- *    cs_buf, cr_buf, out) must be 16-byte aligned; metadata 8-byte; everything else 4-byte.
+ *    cs_buf, cr_buf, out, and the experts' weights and rows: a, w, w1, w2, h, y) must be 16-byte
+ *    aligned; metadata 8-byte; everything else 4-byte.
  *  - Index types are int32.  Rows are addressed as [rank][row] with the row strides given by
  *    moe_sizes().  Every buffer must be the full size moe_sizes() gives, also for a call on a
  *    rank range: the row-copy kernels may read the first row of their source buffer (for lanes
@@ -274,8 +275,9 @@ int moe_combine_acc_send(const moe_shape* shape, const uint16_t* expert_y, const
 int moe_combine_acc_recv(const moe_shape* shape, const uint16_t* cr_buf, const int32_t* topk_idx,
                          const int32_t* send_pos, uint16_t* out, void* stream);
 
-/* Stand-in for the grouped GEMM between dispatch and combine (not part of dispatch/combine;
- * [EFA] overview: the grouped GEMM multiplies tokens by expert weights in between).
+/* Stand-in for the grouped GEMM between dispatch and combine, for runs without weights (the product
+ * itself: moe_expert_mlp below; [EFA] overview: the grouped GEMM multiplies tokens by expert weights
+ * in between).
  *   mode 0 (identity): y = the dispatched value (bf16 as is; e4m3 decoded times its block
  *          scale, rounded once to bf16)
  *   mode 1 (tagged):   y = bf16(that value * (64 + e % 64) / 64) for the row's expert e
@@ -284,6 +286,67 @@ int moe_combine_acc_recv(const moe_shape* shape, const uint16_t* cr_buf, const i
 int moe_expert_stub(const moe_shape* shape, int32_t mode, const void* expert_x,
                     const float* expert_scale, const int32_t* expert_off, uint16_t* expert_y,
                     void* stream);
+
+/* The experts' products: the grouped GEMM between dispatch and combine ([EFA] overview: the grouped
+ * GEMM multiplies tokens by expert weights in between; [PORT] Dispatch: the receiver's contiguous
+ * buffers feed it).  Both layouts.  Expert e = d*L + l of rank d owns rows expert_off[d][l] ..
+ * expert_off[d][l+1] of the rank's B rows, as moe_dispatch_recv and moe_prefill_dispatch lay them
+ * out; an expert may own none.  Rows that no expert owns are not written.  The operands' type is that of
+ * the dispatched rows: bf16 (MOE_BF16), or e4m3 with block scales (the other two).  Rows of one
+ * expert meet only its own matrix, each row on its own: a NaN or infinity stays in its row.  A row's
+ * result does not depend on the other rows' values, and the same call gives the same bits each time.
+ * expert_off entries that are no offsets of B rows set MOE_EINVAL in the status word; their expert
+ * owns no rows then.  Weights are full-size [E][...] arrays also for a call on a rank range.
+ * Operands must not overlap outputs.  No workspace.
+ *   MOE_EUNSUPPORTED  K or C not a multiple of 8 (e4m3: K of 128; the gated product also C of 128),
+ *                     or over 2^20
+ *   MOE_EINVAL        also a scale pointer that is missing (e4m3) or given (bf16) */
+
+/* y = a . w[e]^T for the rows of every expert: one matrix of C rows of K values an expert.  With
+ * N = E = R = 1 and expert_off = {0, rows} it is the plain product of a shared expert.
+ *   a        bf16[N][B][K], or e4m3 u8[N][B][K]
+ *   a_scale  f32[N][B][K/128] (e4m3), else NULL
+ *   w        bf16[E][C][K], or e4m3 u8[E][C][K]
+ *   w_scale  f32[E][ceil(C/128)][K/128] (e4m3: a scale for each block of 128 x 128), else NULL
+ *   y        bf16[N][B][C] (out)   bf16: fp32 sums over k, rounded once (nearest even).  e4m3: per
+ *                                   128 values of k an fp32 sum of the codes' products, times
+ *                                   a_scale * w_scale, added up in fp32 and rounded once */
+int moe_expert_gemm(const moe_shape* shape, int32_t K, int32_t C, const void* a, const float* a_scale,
+                    const void* w, const float* w_scale, const int32_t* expert_off, uint16_t* y,
+                    void* stream);
+
+/* The gated half of an expert's MLP (SwiGLU): g and u are the products of moe_expert_gemm with the
+ * first and the last I rows of w, in fp32, and h = g / (1 + exp(-g)) * u.
+ *   a, a_scale   as for moe_expert_gemm
+ *   w            [E][2I][K], w_scale f32[E][2I/128][K/128] (e4m3): gate rows, then up rows
+ *   h            bf16[N][B][I] (out), h rounded once; or e4m3 u8[N][B][I] (out)
+ *   h_scale      f32[N][B][I/128] (out, e4m3), else NULL.  The e4m3 h is quantised from the fp32
+ *                values by the rule of MOE_BF16_TO_FP8 (amax / 448 per 128 values, 1.0 for zeros);
+ *                a NaN keeps a NaN code */
+int moe_expert_gated(const moe_shape* shape, int32_t K, int32_t I, const void* a, const float* a_scale,
+                     const void* w, const float* w_scale, const int32_t* expert_off, void* h,
+                     float* h_scale, void* stream);
+
+/* Bytes of the weights and of the intermediate rows of moe_expert_mlp for a shape and an
+ * intermediate size I. */
+typedef struct {
+    int64_t w1, w1_scale, w2, w2_scale, h, h_scale;
+} moe_expert_sizes_t;
+
+/* Host only; no GPU needed. */
+int moe_expert_sizes(const moe_shape* shape, int32_t I, moe_expert_sizes_t* out);
+
+/* What stands between dispatch and combine: = moe_expert_gated with K = H, then moe_expert_gemm of
+ * its rows with K = I and C = H (all arguments validated first).
+ *   expert_x, expert_scale, expert_off   from moe_dispatch_recv or moe_prefill_dispatch
+ *   w1 [E][2I][H], w1_scale f32[E][2I/128][H/128] (e4m3); w2 [E][H][I], w2_scale
+ *   f32[E][H/128][I/128] (e4m3)
+ *   h, h_scale   [N][B][I], f32[N][B][I/128] (e4m3) (out)   the gated rows
+ *   expert_y     bf16[N][B][H] (out)   for moe_combine, moe_combine_acc and moe_prefill_combine */
+int moe_expert_mlp(const moe_shape* shape, int32_t I, const void* expert_x, const float* expert_scale,
+                   const void* w1, const float* w1_scale, const void* w2, const float* w2_scale,
+                   const int32_t* expert_off, void* h, float* h_scale, uint16_t* expert_y,
+                   void* stream);
 
 /* Prefill dispatch (MOE_LAYOUT_PREFILL).  [QWEN] MoE dispatch-combine, Expert parallel: the
  * inputs are replicated on every rank, so each rank's dispatch only selects the tokens routed to
