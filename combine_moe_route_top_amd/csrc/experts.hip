@@ -31,18 +31,52 @@ struct Product {
     int L, rb, rc;
 };
 
-constexpr int kStepBytes = 128;   // of every row, per step over K: 64 bf16 or 128 e4m3 values
-constexpr int kMaxExperts = 1024; // of all ranks
-constexpr int kThreads = 256;
+constexpr int kStepBytes = 128;    // of every row, per step over K: 64 bf16 or 128 e4m3 values
+constexpr int kMaxExperts = 1024;  // of all ranks
+constexpr int kCUs = 256;
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * kWave;
+constexpr int kRingBytes = 150 << 10;
+constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before the next one
 
 // A chunk of zeros: what lanes past the end of a row load in its last step.
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+// The shape of a tile: BM rows x BN weight rows by WM x WN x KP waves (KP: waves that share a
+// tile's part and take every KP-th step), through a ring of S stages of KP steps each.
+template <int BM_, int BN_, int WM_, int WN_, int KP_, int S_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KP = KP_, S = S_;
+    static_assert(WM * WN * KP == kWaves, "eight waves");
+    static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 parts of a wave
+    static constexpr int kFillsPerStep = (BM + BN) / 8;         // loads of 8 rows
+    static constexpr int kFills = KP * kFillsPerStep;
+    static constexpr int kPerWave = (kFills + kWaves - 1) / kWaves;
+    static constexpr int kTileBytes = KP * (BM + BN) * kStepBytes;
+    // the scales of a stage (e4m3): a row of kThreads floats; KP steps of BM + 2 of them are used
+    template <bool FP8>
+    static constexpr int stage() { return kTileBytes + (FP8 ? kThreads * 4 : 0); }
+    static_assert(S * (kTileBytes + kThreads * 4) <= kRingBytes, "the ring");
+    static_assert(KP * (BM + 2) <= kThreads, "a stage's scales");
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A barrier that waits for the wave's LDS accesses but not for its loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void load_lds4(const float* src, float* dst) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 4, 0, 0);
+
+// Waits until at most N of the wave's loads and stores are in flight (loads end in order).  Not the
+// builtin: after __builtin_amdgcn_s_waitcnt(vmcnt(0)) the compiler made the LDS reads of the
+// two-stage ring wait for the loads issued since, which the other stage receives.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // Rows of expert x of the call (x counts over its ranks' local experts): the first row within the
@@ -72,198 +106,438 @@ __device__ __forceinline__ uint32_t e4m3_code(float v) {
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
-// A block computes tiles of BM = 16 MT rows x BN = 16 NT WN weight rows with WN waves side by side
-// along the weight rows.  The matrix instruction takes the weights as its first operand, so that a
-// lane holds four neighbouring output columns of one row, and its row's scale is one number.  For
-// the gated product the tile's weight rows alternate, 16 gate rows and 16 up rows, so that both
-// factors of a column meet in the same register index of the same lane.
-template <bool FP8, bool GATED, int MT, int NT, int WN>
-__global__ __launch_bounds__(64 * WN) void k_experts(Product P) {
-    constexpr int BM = 16 * MT, BN = 16 * NT * WN, T = 64 * WN;
-    constexpr int kCols = GATED ? BN / 2 : BN;  // output columns of a tile
-    __shared__ __attribute__((aligned(16))) uint8_t tile[(BM + BN) * kStepBytes];
-    __shared__ float scl[T];
-    __shared__ int base[kMaxExperts + 1];
-    __shared__ float amax_of[WN][BM];
-    const int lane = lane_id(), wave = wave_id();
-    const int X = P.rc * P.L;
-    const int ntn = (P.C + kCols - 1) / kCols;
-    // tiles before each expert's
-    for (int x = threadIdx.x; x < X; x += T) {
-        int first;
-        base[x] = (expert_rows(P, x, &first) + BM - 1) / BM;
+// What tile t is of: its expert's rows and matrix, and where in them it lies.
+struct Place {
+    int cnt, m0, n0;
+    long row0;  // the expert's first row in the row arrays
+    long e;
+};
+
+template <class T, bool GATED>
+__device__ __forceinline__ Place place_of(const Product& P, const int* base, int X, int ntn, int t) {
+    // the last expert with base[x] <= q: 16 at a time, then one by one
+    const int q = t / ntn, lane = lane_id();
+    int i = lane * 16;
+    const int c = __popcll(ballot(i < X && base[i < X ? i : 0] <= q)) - 1;
+    i = c * 16 + lane;
+    const int x = c * 16 + __popcll(ballot(lane < 16 && i < X && base[i < X ? i : 0] <= q)) - 1;
+    const int b0 = uniform(base[x]), mts = uniform(base[x + 1]) - b0;
+    // row tiles in groups: within a group every row tile meets a weight tile before the next one
+    // comes, so that both stay in the XCD's cache while its CUs use them
+    const int in = t - b0 * ntn, g = in / (kGroupTiles * ntn), r = in - g * kGroupTiles * ntn;
+    const int left = mts - g * kGroupTiles, gm = left < kGroupTiles ? left : kGroupTiles;
+    Place p;
+    p.m0 = (g * kGroupTiles + r % gm) * T::BM;
+    p.n0 = r / gm * (GATED ? T::BN / 2 : T::BN);
+    int first;
+    p.cnt = uniform(expert_rows(P, x, &first));
+    const int d = P.rb + x / P.L;
+    p.e = (long)d * P.L + x % P.L;
+    p.row0 = (long)d * P.B + uniform(first);
+    return p;
+}
+
+// Where a wave loads a stage of a tile from: the tile's first row and first weight row (the wave's half
+// of them, if gated), an offset of the lane for each fill, and the lane's scale.
+template <class T>
+struct Source {
+    const uint8_t* rows;
+    const uint8_t* weights;
+    uint32_t off[T::kPerWave];
+    const float* scale;
+};
+
+// Fill i = wave + 8 j of a stage brings rows 8 (i % kFillsPerStep) .. + 7 of step i / kFillsPerStep.
+template <class T>
+struct Fill {
+    int kp, r;  // step; first of its rows: BM rows, then BN weight rows
+    __device__ __forceinline__ Fill(int wave, int j) {
+        const int i = (wave & 7) + j * kWaves;
+        kp = T::KP == 1 ? 0 : i / T::kFillsPerStep;
+        r = (i - kp * T::kFillsPerStep) * 8;
     }
-    __syncthreads();
-    if (wave == 0) wave_excl_scan_array(base, base, X);
-    __syncthreads();
-    const long tiles = (long)base[X] * ntn;
-    for (long t = blockIdx.x; t < tiles; t += gridDim.x) {
-        // the expert whose tiles hold t: the last with base[x] * ntn <= t
-        int x = 0;
-        for (int s = 512; s > 0; s >>= 1)
-            if (x + s < X && (long)base[x + s] * ntn <= t) x += s;
-        const long in = t - (long)base[x] * ntn;
-        const int mts = base[x + 1] - base[x];
-        const int n0 = (int)(in / mts) * kCols, m0 = (int)(in % mts) * BM;
-        int first;
-        const int cnt = expert_rows(P, x, &first);
-        const int d = P.rb + x / P.L;
-        const long e = (long)d * P.L + x % P.L;
-        const long row0 = (long)d * P.B + first;
-        const int wrows = GATED ? 2 * P.C : P.C;
-        const uint8_t* w = P.w + e * wrows * P.KB;
+};
 
-        f32x4 acc[NT][MT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(const float* src, float* dst) {
+    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 4, 0, 0);
+}
 
-        const int steps = (P.KB + kStepBytes - 1) / kStepBytes;
-        for (int k = 0; k < steps; ++k) {
-            // lane l of an instruction that fills rows 8i .. 8i+7 lands at row l/8, place l%8; it
-            // fetches the row's 16-byte chunk (l%8) ^ (l/8), so that the reads below spread over the
-            // LDS banks
-            const int chunk = (lane & 7) ^ (lane >> 3);
-            const int kb = k * kStepBytes + chunk * 16;
-            for (int i = wave; i < (BM + BN) / 8; i += WN) {
-                const int r = i * 8 + (lane >> 3);
-                const uint8_t* src;
-                if (r < BM) {
-                    const int m = m0 + r < cnt ? m0 + r : cnt - 1;
-                    src = P.a + (row0 + m) * P.KB + kb;
-                } else {
-                    const int q = r - BM;
-                    int c = GATED ? n0 + (q >> 5) * 16 + (q & 15) : n0 + q;
-                    c = c < P.C ? c : P.C - 1;
-                    src = w + (long)(GATED && (q & 16) ? P.C + c : c) * P.KB + kb;
-                }
-                load_lds16(kb < P.KB ? src : kZeros, tile + i * 1024);
-            }
-            if constexpr (FP8) {
-                // the rows' scales of this step, then the tile's weight blocks'
-                const int i = threadIdx.x;
-                const int m = m0 + i < cnt ? m0 + i : cnt - 1;
-                const float* src = P.as + (row0 + m) * P.KS + k;
-                if (i >= BM) {
-                    const int j = i - BM, blocks = (wrows + 127) / 128;
-                    int b = GATED ? (n0 + (j & 1) * P.C) / 128 : n0 / 128 + j;
-                    b = b < blocks ? b : blocks - 1;
-                    src = P.ws + (e * blocks + b) * P.KS + k;
-                }
-                load_lds4(src, scl + wave * 64);
-            }
-            __syncthreads();
-            const int r16 = lane & 15, g = lane >> 4;
-            float sr[MT], sw[2];
-            if constexpr (FP8) {
+// Lane l of a fill lands at row l / 8, place l % 8, and fetches the row's 16-byte chunk (l % 8) ^ (l / 8):
+// the reads of a 16-row part then spread over the LDS banks.  Rows past an expert's last repeat it;
+// weight rows past the last repeat it too.  For the gated product the weight rows of a tile alternate,
+// 16 gate rows and 16 up rows: a wave's fills, 64 rows apart, are all of one kind.
+template <bool FP8, bool GATED, class T>
+__device__ __forceinline__ void aim(const Product& P, const Place& p, Source<T>& s) {
+    const int lane = lane_id(), wave = uniform(wave_id());
+    const int wrows = GATED ? 2 * P.C : P.C;
+    const int chunk = (lane & 7) ^ (lane >> 3), r8 = lane >> 3;
+    static_assert(T::kFillsPerStep % 4 == 2 ? T::KP == 1 : T::kFillsPerStep % 4 == 0, "a wave's fills are of one kind");
+    const bool up = GATED && ((wave * 8 - T::BM) & 16);
+    s.rows = P.a + (p.row0 + p.m0) * P.KB;
+    s.weights = P.w + (p.e * wrows + p.n0 + (up ? P.C : 0)) * P.KB;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) sr[j] = scl[j * 16 + r16];
-                sw[0] = scl[BM + (GATED ? 0 : wave * NT * 16 / 128)];
-                sw[1] = GATED ? scl[BM + 1] : sw[0];
-            }
-            // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
-            const int p0 = (g ^ (r16 & 7)) * 16, p1 = ((g + 4) ^ (r16 & 7)) * 16;
-            i32x4 b[MT][2];
+    for (int j = 0; j < T::kPerWave; ++j) {
+        const Fill<T> f(wave, j);
+        const int q = f.r - T::BM;
+        const bool tok = q < 0;
+        const int r = (tok ? f.r : GATED ? (q >> 5) * 16 + (q & 15) : q) + r8;
+        const int last = tok ? p.cnt - 1 - p.m0 : P.C - 1 - p.n0;
+        s.off[j] = (uint32_t)(r < last ? r : last) * P.KB + f.kp * kStepBytes + chunk * 16;
+    }
+    if constexpr (FP8) {
+        const int i = threadIdx.x, kp = i / (T::BM + 2), r = i - kp * (T::BM + 2);
+        const int blocks = (wrows + 127) / 128;
+        if (r < T::BM || kp >= T::KP) {
+            const int m = p.m0 + r < p.cnt ? p.m0 + r : p.cnt - 1;
+            s.scale = P.as + (p.row0 + m) * P.KS + (kp < T::KP ? kp : 0);
+        } else {
+            int b = GATED ? (p.n0 + (r - T::BM) * P.C) / 128 : p.n0 / 128 + (r - T::BM);
+            b = b < blocks ? b : blocks - 1;
+            s.scale = P.ws + (p.e * blocks + b) * P.KS + kp;
+        }
+    }
+}
+
+// Loads stage k of the tile that `src` aims at into `wr`.
+template <bool FP8, class T>
+__device__ __forceinline__ void fetch_stage(uint8_t* wr, const Product& P, const Source<T>& src, int k) {
+    const int lane = lane_id(), wave = uniform(wave_id());
+    const int kb = k * T::KP * kStepBytes;
+    const uint8_t *rows = src.rows + kb, *weights = src.weights + kb;
+    if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) {
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const uint8_t* row = tile + (j * 16 + r16) * kStepBytes;
-                b[j][0] = *(const i32x4*)(row + p0);
-                b[j][1] = *(const i32x4*)(row + p1);
+        for (int j = 0; j < T::kPerWave; ++j) {
+            const Fill<T> f(wave, j);
+            if (T::kFills % kWaves == 0 || wave + j * kWaves < T::kFills)
+                load_lds16((f.r < T::BM ? rows : weights) + src.off[j], wr + (wave + j * kWaves) * 1024);
+        }
+    } else {  // the last stage of a row: zeros from the row's end on
+        const int chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+        for (int j = 0; j < T::kPerWave; ++j) {
+            const Fill<T> f(wave, j);
+            uint32_t off = src.off[j];
+            asm volatile("" : "+v"(off));  // keeps this path's addresses out of the other's registers
+            const bool in = kb + f.kp * kStepBytes + chunk * 16 < P.KB;
+            if (T::kFills % kWaves == 0 || wave + j * kWaves < T::kFills)
+                load_lds16(in ? (f.r < T::BM ? rows : weights) + off : kZeros, wr + (wave + j * kWaves) * 1024);
+        }
+    }
+    if constexpr (FP8) {
+        // a step past the last reads the row's last scale (its codes are zeros)
+        const int kp = threadIdx.x / (T::BM + 2);
+        const int ks = k * T::KP, over = ks + (kp < T::KP ? kp : 0) - (P.KS - 1);
+        load_lds4(src.scale + ks - (over > 0 ? over : 0), (float*)(wr + T::kTileBytes) + wave * 64);
+    }
+}
+
+// One stage: the loads of stage k of a tile into `wr` (if `fetch`), and the products of the stage in
+// `rd`.  The two never overlap; saying so (__restrict__ on both) keeps the compiler from making the
+// reads wait for the loads.
+template <bool FP8, bool GATED, class T>
+__device__ __forceinline__ void stage_step(const uint8_t* __restrict__ rd, uint8_t* __restrict__ wr, const Product& P,
+                                           const Source<T>& src, int k, bool fetch, f32x4 (&acc)[T::NT][T::MT]) {
+    constexpr int MT = T::MT, NT = T::NT;
+    const int lane = lane_id(), wave = uniform(wave_id());
+    if (fetch) fetch_stage<FP8, T>(wr, P, src, k);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
+    float sr[MT], sw[2];
+    if constexpr (FP8) {
+        const float* scl = (const float*)(rd + T::kTileBytes) + kp * (T::BM + 2);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sr[j] = scl[(wm * MT + j) * 16 + r16];
+        sw[0] = scl[T::BM + (GATED ? 0 : wn * NT * 16 / 128)];
+        sw[1] = GATED ? scl[T::BM + 1] : sw[0];
+    }
+    // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
+    const int p0 = (g ^ (r16 & 7)) * 16, p1 = p0 ^ 64;
+    const uint8_t* ta = rd + (kp * (T::BM + T::BN) + wm * MT * 16 + r16) * kStepBytes;
+    const uint8_t* tw = rd + (kp * (T::BM + T::BN) + T::BM + wn * NT * 16 + r16) * kStepBytes;
+    i32x4 w[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        w[i][0] = *(const i32x4*)(tw + i * 16 * kStepBytes + p0);
+        w[i][1] = *(const i32x4*)(tw + i * 16 * kStepBytes + p1);
+    }
+    i32x4 b[2][2];
+    b[0][0] = *(const i32x4*)(ta + p0);
+    b[0][1] = *(const i32x4*)(ta + p1);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        // the next part's rows are read while this one's products run; no further ahead, for the
+        // registers' sake
+        if (j + 1 < MT) {
+            b[(j + 1) & 1][0] = *(const i32x4*)(ta + (j + 1) * 16 * kStepBytes + p0);
+            b[(j + 1) & 1][1] = *(const i32x4*)(ta + (j + 1) * 16 * kStepBytes + p1);
+        }
+        const i32x4 b0 = b[j & 1][0], b1 = b[j & 1][1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if constexpr (FP8) {
+                const i32x8 A = __builtin_shufflevector(w[i][0], w[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+                const f32x4 p =
+                    __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                const float s = sr[j] * sw[GATED ? (i & 1) : 0];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], s, acc[i][j][v]);
+                // here, and not after all products: the partial sums would need registers of their own
+                asm volatile("" : "+v"(acc[i][j]));
+            } else {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w[i][0]), __builtin_bit_cast(bf16x8, b0), acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w[i][1]), __builtin_bit_cast(bf16x8, b1), acc[i][j], 0, 0, 0);
             }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// A tile's results: the lane's row of each 16-row part, four neighbouring columns of each 16-column
+// part.  `epi`: LDS apart from the ring.
+template <bool FP8, bool GATED, class T>
+__device__ __forceinline__ void write_tile(const Product& P, const Place& p, f32x4 (&acc)[T::NT][T::MT], float* epi) {
+    constexpr int MT = T::MT, NT = T::NT;
+    const int lane = lane_id(), wave = uniform(wave_id());
+    const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
+    const int r16 = lane & 15, c4 = (lane >> 4) * 4;
+    if constexpr (T::KP > 1) {
+        // the waves of a part add up in their order: each of the others leaves its sums for the first
+        f32x4* mine = (f32x4*)epi + wave % (T::WM * T::WN) * NT * MT * kWave;
+        for (int q = 1; q < T::KP; ++q) {
+            if (kp == q) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) mine[(i * MT + j) * kWave + lane] = acc[i][j];
+            }
+            lds_barrier();
+            if (kp == 0) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) acc[i][j] += mine[(i * MT + j) * kWave + lane];
+            }
+            lds_barrier();
+        }
+    }
+    const bool writes = kp == 0;
+    if constexpr (!GATED) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int m = p.m0 + (wm * MT + j) * 16 + r16;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const uint8_t* row = tile + (BM + (wave * NT + i) * 16 + r16) * kStepBytes;
-                const i32x4 a0 = *(const i32x4*)(row + p0), a1 = *(const i32x4*)(row + p1);
-#pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    if constexpr (FP8) {
-                        const i32x8 A = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-                        const i32x8 Bv = __builtin_shufflevector(b[j][0], b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            A, Bv, f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-                        const float s = sr[j] * sw[GATED ? (i & 1) : 0];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], s, acc[i][j][v]);
-                    } else {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, a0), __builtin_bit_cast(bf16x8, b[j][0]), acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, a1), __builtin_bit_cast(bf16x8, b[j][1]), acc[i][j], 0, 0, 0);
-                    }
-                }
+                const int c = p.n0 + (wn * NT + i) * 16 + c4;
+                if (!writes || m >= p.cnt || c >= P.C) continue;
+                uint2 v;
+                v.x = f32_to_bf16(acc[i][j][0]) | f32_to_bf16(acc[i][j][1]) << 16;
+                v.y = f32_to_bf16(acc[i][j][2]) | f32_to_bf16(acc[i][j][3]) << 16;
+                *(uint2*)(P.out + ((p.row0 + m) * P.C + c) * 2) = v;
             }
-            __syncthreads();
         }
-        // epilogue: the lane's row of each 16-row group, four columns of each 16-column group
-        const int r16 = lane & 15, c4 = (lane >> 4) * 4;
-        if constexpr (!GATED) {
+    } else {
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int i = 0; i < NT; i += 2)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = swiglu(acc[i][j][v], acc[i + 1][j][v]);
+        if constexpr (FP8) {
+            static_assert(T::BN == 256 && T::KP == 1, "a tile holds a whole block of 128 columns");
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                const int m = m0 + j * 16 + r16;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int c = n0 + (wave * NT + i) * 16 + c4;
-                    if (m >= cnt || c >= P.C) continue;
-                    uint2 v;
-                    v.x = f32_to_bf16(acc[i][j][0]) | f32_to_bf16(acc[i][j][1]) << 16;
-                    v.y = f32_to_bf16(acc[i][j][2]) | f32_to_bf16(acc[i][j][3]) << 16;
-                    *(uint2*)(P.out + ((row0 + m) * P.C + c) * 2) = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
+                float m = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NT; i += 2)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[i][j][v] = swiglu(acc[i][j][v], acc[i + 1][j][v]);
+                    for (int v = 0; v < 4; ++v) m = fmaxf(m, fabsf(acc[i][j][v]));
+                m = fmaxf(m, __shfl_xor(m, 16, kWave));
+                m = fmaxf(m, __shfl_xor(m, 32, kWave));
+                if (lane < 16) epi[wn * T::BM + (wm * MT + j) * 16 + lane] = m;
+            }
+            lds_barrier();
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int m = p.m0 + (wm * MT + j) * 16 + r16;
+            float sc = 1.0f;
             if constexpr (FP8) {
+                float a = 0.0f;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < NT; i += 2)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) m = fmaxf(m, fabsf(acc[i][j][v]));
-                    m = fmaxf(m, __shfl_xor(m, 16, kWave));
-                    m = fmaxf(m, __shfl_xor(m, 32, kWave));
-                    if (lane < 16) amax_of[wave][j * 16 + lane] = m;
-                }
-                __syncthreads();
+                for (int q = 0; q < T::WN; ++q) a = fmaxf(a, epi[q * T::BM + (wm * MT + j) * 16 + r16]);
+                sc = a > 0.0f ? a / 448.0f : 1.0f;
+                if (wn == 0 && lane < 16 && m < p.cnt) P.out_scale[(p.row0 + m) * (P.C / 128) + p.n0 / 128] = sc;
             }
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const int m = m0 + j * 16 + r16;
-                float sc = 1.0f;
+            for (int i = 0; i < NT; i += 2) {
+                const int c = p.n0 + (wn * NT + i) * 8 + c4;
+                if (!writes || m >= p.cnt || c >= P.C) continue;
+                const f32x4 h = acc[i][j];
                 if constexpr (FP8) {
-                    float a = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < WN; ++q) a = fmaxf(a, amax_of[q][j * 16 + r16]);
-                    sc = a > 0.0f ? a / 448.0f : 1.0f;
-                    if (wave == 0 && lane < 16 && m < cnt)
-                        P.out_scale[(row0 + m) * (P.C / 128) + n0 / 128] = sc;
-                }
-#pragma unroll
-                for (int i = 0; i < NT; i += 2) {
-                    const int c = n0 + (wave * NT + i) * 8 + c4;
-                    if (m >= cnt || c >= P.C) continue;
-                    const f32x4 h = acc[i][j];
-                    if constexpr (FP8) {
-                        *(uint32_t*)(P.out + (row0 + m) * P.C + c) =
-                            e4m3_code(h[0] / sc) | e4m3_code(h[1] / sc) << 8 | e4m3_code(h[2] / sc) << 16 |
-                            e4m3_code(h[3] / sc) << 24;
-                    } else {
-                        uint2 v;
-                        v.x = f32_to_bf16(h[0]) | f32_to_bf16(h[1]) << 16;
-                        v.y = f32_to_bf16(h[2]) | f32_to_bf16(h[3]) << 16;
-                        *(uint2*)(P.out + ((row0 + m) * P.C + c) * 2) = v;
-                    }
+                    *(uint32_t*)(P.out + (p.row0 + m) * P.C + c) = e4m3_code(h[0] / sc) | e4m3_code(h[1] / sc) << 8 |
+                                                                   e4m3_code(h[2] / sc) << 16 |
+                                                                   e4m3_code(h[3] / sc) << 24;
+                } else {
+                    uint2 v;
+                    v.x = f32_to_bf16(h[0]) | f32_to_bf16(h[1]) << 16;
+                    v.y = f32_to_bf16(h[2]) | f32_to_bf16(h[3]) << 16;
+                    *(uint2*)(P.out + ((p.row0 + m) * P.C + c) * 2) = v;
                 }
             }
-            if constexpr (FP8) __syncthreads();
+        }
+        if constexpr (FP8) lds_barrier();  // the next tile's maxima
+    }
+}
+
+// The block's tiles, v, v + G, ..., as one run of stages: the loads run S - 1 stages ahead of the
+// products, across the ends of tiles.
+template <bool FP8, bool GATED, class T>
+__device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const int* base, float* epi, int X, int v,
+                                          int G) {
+    constexpr int kStage = T::template stage<FP8>(), S = T::S;
+    constexpr int kLoads = T::kPerWave + (FP8 ? 1 : 0);  // of a stage, at most
+    // waves with fewer fills than others wait for one stage more than they need
+    constexpr int kFew = T::kFills / kWaves + (FP8 ? 1 : 0);
+    const int ntn = (P.C + (GATED ? T::BN / 2 : T::BN) - 1) / (GATED ? T::BN / 2 : T::BN);
+    const int tiles = base[X] * ntn;
+    if (v >= tiles) return;
+    const int stages = (P.KB + T::KP * kStepBytes - 1) / (T::KP * kStepBytes);
+    const long total = (long)((tiles - 1 - v) / G + 1) * stages;
+    const bool many = uniform(wave_id()) < T::kFills % kWaves;
+    f32x4 acc[T::NT][T::MT];
+    Source<T> src;
+    Place p = place_of<T, GATED>(P, base, X, ntn, v);
+    aim<FP8, GATED, T>(P, p, src);
+    int lt = v, lk = 0, ct = v, ck = 0;  // tile and stage of the loads and of the products
+    int rslot = 0, wslot = 0;
+    auto zero = [&] {
+#pragma unroll
+        for (int i = 0; i < T::NT; ++i)
+#pragma unroll
+            for (int j = 0; j < T::MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    };
+    zero();
+    auto advance = [&] {
+        ++lk;
+        wslot = wslot == S - 1 ? 0 : wslot + 1;
+        if (lk == stages) {
+            lk = 0;
+            lt += G;
+            if (lt < tiles) aim<FP8, GATED, T>(P, place_of<T, GATED>(P, base, X, ntn, lt), src);
+        }
+    };
+    for (int n = 0; n < S - 1 && n < total; ++n) {
+        fetch_stage<FP8, T>(ring + wslot * kStage, P, src, lk);
+        advance();
+    }
+    for (long n = 0; n < total; ++n) {
+        if (n + S - 1 <= total) {
+            if (T::kFills % kWaves && many) wait_loads<(S - 2) * kLoads>();
+            else wait_loads<(S - 2) * (T::kFills % kWaves ? kFew : kLoads)>();
+        } else {
+            wait_loads<0>();
+        }
+        lds_barrier();
+        const bool fetch = n + S - 1 < total;
+        stage_step<FP8, GATED, T>(ring + rslot * kStage, ring + wslot * kStage, P, src, lk, fetch, acc);
+        rslot = rslot == S - 1 ? 0 : rslot + 1;
+        if (fetch) advance();
+        if (++ck == stages) {
+            p = place_of<T, GATED>(P, base, X, ntn, ct);
+            write_tile<FP8, GATED, T>(P, p, acc, epi);
+            zero();
+            ck = 0;
+            ct += G;
         }
     }
+    lds_barrier();
+}
+
+// The tiles of experts by their rows.
+typedef Tile<16, 256, 1, 8, 1, 4> Tile16;
+typedef Tile<32, 256, 1, 8, 1, 3> Tile32;
+typedef Tile<64, 256, 1, 8, 1, 3> Tile64;
+typedef Tile<128, 256, 2, 4, 1, 3> Tile128;
+typedef Tile<256, 256, 2, 4, 1, 2> Tile256;
+
+#ifndef MOE_EXPERT_CLASS
+#define MOE_EXPERT_CLASS -1
+#endif
+__device__ __forceinline__ int class_of(int rows) {
+    if (MOE_EXPERT_CLASS >= 0) return MOE_EXPERT_CLASS;
+    return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 3 : 4;
+}
+
+// base[x] = row tiles of the experts before x that are of the class; tiles of BM rows.
+__device__ __forceinline__ void scan_tiles(const int* rows, int cls, int BM, int X, int* base, int* part) {
+    lds_barrier();  // the last class is done with base
+    int n[2], v = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = 2 * threadIdx.x + i;
+        n[i] = x < X && class_of(rows[i]) == cls ? (rows[i] + BM - 1) / BM : 0;
+        v += n[i];
+    }
+    const int inc = wave_incl_scan(v);
+    if (lane_id() == kWave - 1) part[wave_id()] = inc;
+    lds_barrier();
+    int before = inc - v;
+    for (int w = 0; w < wave_id(); ++w) before += part[w];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = 2 * threadIdx.x + i;
+        if (x <= X) base[x] = before;
+        before += n[i];
+    }
+    if (threadIdx.x == kThreads - 1) base[kMaxExperts] = before;
+    lds_barrier();
+}
+
+template <bool FP8, bool GATED>
+__global__ __launch_bounds__(kThreads) void k_experts(Product P) {
+    __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes];
+    __shared__ __attribute__((aligned(16))) float epi[1024];
+    __shared__ int base[kMaxExperts + 1];
+    __shared__ int part[kWaves];
+    __shared__ int present;
+    const int X = P.rc * P.L, G = gridDim.x;
+    // blocks of one XCD (the hardware deals blocks to the eight in turn) take neighbouring tiles
+    const int per = G / 8, b = blockIdx.x;
+    const int v = b < per * 8 ? b % 8 * per + b / 8 : b;
+    if (threadIdx.x == 0) present = 0;
+    lds_barrier();
+    int rows[2] = {0, 0}, first, bits = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int x = 2 * threadIdx.x + i;
+        if (x < X) rows[i] = expert_rows(P, x, &first);
+        if (rows[i] > 0) bits |= 1 << class_of(rows[i]);
+    }
+    if (bits) atomicOr(&present, bits);
+    lds_barrier();
+    const int all = uniform(present);
+    int done = 0;  // tiles of the classes before: the next class begins at the block after them
+    auto run = [&](auto tile, int cls) {
+        typedef decltype(tile) T;
+        if (!(all >> cls & 1)) return;
+        scan_tiles(rows, cls, T::BM, X, base, part);
+        int w = v - done % G;
+        w = w < 0 ? w + G : w;
+        run_tiles<FP8, GATED, T>(P, ring, base, epi, X, w, G);
+        const int cols = GATED ? T::BN / 2 : T::BN;
+        done += uniform(base[X]) * ((P.C + cols - 1) / cols);
+    };
+    if (MOE_EXPERT_CLASS < 0 || MOE_EXPERT_CLASS == 4) run(Tile256(), 4);
+    if (MOE_EXPERT_CLASS < 0 || MOE_EXPERT_CLASS == 3) run(Tile128(), 3);
+    if (MOE_EXPERT_CLASS < 0 || MOE_EXPERT_CLASS == 2) run(Tile64(), 2);
+    if (MOE_EXPERT_CLASS < 0 || MOE_EXPERT_CLASS == 1) run(Tile32(), 1);
+    if (MOE_EXPERT_CLASS < 0 || MOE_EXPERT_CLASS == 0) run(Tile16(), 0);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -288,15 +562,15 @@ hipError_t launch_experts(const Dims& D, bool gated, int K, int C, const void* a
     P.L = D.L;
     P.rb = D.rb;
     P.rc = D.rc;
-    constexpr int MT = 4, NT = 4, WN = 4;
-    const long mts = (recv_rows_bound(D) + 16 * MT - 1) / (16 * MT) + (long)D.rc * D.L;
-    const int cols = gated ? 8 * NT * WN : 16 * NT * WN;
+    // one block a CU (each takes nearly all of its LDS); fewer if there cannot be as many tiles
+    const long mts = (recv_rows_bound(D) + 15) / 16 + (long)D.rc * D.L;
+    const int cols = gated ? 128 : 256;
     const long tiles = mts * ((C + cols - 1) / cols);
-    const dim3 grid((unsigned)(tiles < 1024 ? tiles : 1024)), block(64 * WN);
-    if (D.fp8 && gated) hipLaunchKernelGGL((k_experts<true, true, MT, NT, WN>), grid, block, 0, st, P);
-    else if (D.fp8) hipLaunchKernelGGL((k_experts<true, false, MT, NT, WN>), grid, block, 0, st, P);
-    else if (gated) hipLaunchKernelGGL((k_experts<false, true, MT, NT, WN>), grid, block, 0, st, P);
-    else hipLaunchKernelGGL((k_experts<false, false, MT, NT, WN>), grid, block, 0, st, P);
+    const dim3 grid((unsigned)(tiles < kCUs ? tiles : kCUs)), block(kThreads);
+    if (D.fp8 && gated) hipLaunchKernelGGL((k_experts<true, true>), grid, block, 0, st, P);
+    else if (D.fp8) hipLaunchKernelGGL((k_experts<true, false>), grid, block, 0, st, P);
+    else if (gated) hipLaunchKernelGGL((k_experts<false, true>), grid, block, 0, st, P);
+    else hipLaunchKernelGGL((k_experts<false, false>), grid, block, 0, st, P);
     return hipGetLastError();
 }
 
