@@ -36,7 +36,7 @@ constexpr int kMaxExperts = 1024;  // of all ranks
 constexpr int kCUs = 256;
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
-constexpr int kRingBytes = 150 << 10;
+constexpr int kRingBytes = 147200;
 constexpr int kEpiBytes = 4 << 10;
 constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before the next one
 
@@ -44,20 +44,31 @@ constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before 
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
 // The shape of a tile: BM rows x BN weight rows by WM x WN x KP waves (KP: waves that share a
-// tile's part and take every KP-th step), through a ring of S stages of KP steps each.
-template <int BM_, int BN_, int WM_, int WN_, int KP_, int S_>
+// tile's part and take every KP-th step).  A stage is KP steps.  The rows go through a ring of SR
+// stages, loaded by the first waves, the weights through one of SW, loaded by the last four: a wave
+// waits for its loads in their order, so rows (short way, from the cache) and weights (long way, from
+// memory) wait apart.  EARLY: a stage's weights are read into registers at its begin and their place
+// refilled at once, not after the stage.
+template <int BM_, int BN_, int WM_, int WN_, int KP_, int SR_, int SW_, bool EARLY_ = false>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KP = KP_, S = S_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KP = KP_, SR = SR_, SW = SW_;
+    static constexpr bool EARLY = EARLY_;
     static_assert(WM * WN * KP == kWaves, "eight waves");
     static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 parts of a wave
-    static constexpr int kFillsPerStep = (BM + BN) / 8;         // loads of 8 rows
-    static constexpr int kFills = KP * kFillsPerStep;
-    static constexpr int kPerWave = (kFills + kWaves - 1) / kWaves;
-    static constexpr int kTileBytes = KP * (BM + BN) * kStepBytes;
-    // the scales of a stage (e4m3): a row of kThreads floats; KP steps of BM + 2 of them are used
+    // waves that load rows and weights, and the loads of 8 rows of each, a stage
+    static constexpr int kRowFills = KP * BM / 8, kWeightFills = KP * BN / 8;
+    static constexpr int WR = kRowFills < 4 ? kRowFills : 4, WW = 4;
+    static constexpr int FR = kRowFills / WR, FW = kWeightFills / WW, F = FR > FW ? FR : FW;
+    static_assert(FR * WR == kRowFills && FW * WW == kWeightFills, "whole fills");
+    // stages that the loads run ahead
+    static constexpr int kRowLead = SR - 1, kWeightLead = EARLY ? SW : SW - 1;
+    static constexpr int kRowSlot = KP * BM * kStepBytes, kWeightSlot = KP * BN * kStepBytes;
+    // e4m3: the scales of four steps, 16 bytes for each row and for the tile's two weight blocks
+    static constexpr int kScaleLoads = (BM + 2 + kWave - 1) / kWave, kScaleSlot = kScaleLoads * kWave * 16;
+    static_assert(4 % KP == 0 || KP == 8, "whole stages of scales");
+    static constexpr int kWeightsAt = SR * kRowSlot, kScalesAt = kWeightsAt + SW * kWeightSlot;
     template <bool FP8>
-    static constexpr int stage() { return kTileBytes + (FP8 ? kThreads * 4 : 0); }
-    static_assert(KP * (BM + 2) <= kThreads, "a stage's scales");
+    static constexpr int bytes() { return kScalesAt + (FP8 ? SR * kScaleSlot : 0); }
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -114,22 +125,28 @@ struct Place {
     long e;
 };
 
+// Of each expert of the call, in LDS: row tiles before it, first row, rows.
+struct Experts {
+    int base[kMaxExperts + 1];
+    int first[kMaxExperts];
+    int rows[kMaxExperts];
+};
+
 template <class T, bool GATED>
-__device__ __forceinline__ Place place_of(const Product& P, const int* base, int X, int ntn, int t) {
+__device__ __forceinline__ Place place_of(const Product& P, const Experts& E, int X, int ntn, int t) {
     // the last expert with base[x] <= q: 16 at a time, then one by one
     const int q = t / ntn, lane = lane_id();
     int i = lane * 16;
-    const int c = __popcll(ballot(i < X && base[i < X ? i : 0] <= q)) - 1;
+    const int c = __popcll(ballot(i < X && E.base[i < X ? i : 0] <= q)) - 1;
     i = c * 16 + lane;
-    const int x = c * 16 + __popcll(ballot(lane < 16 && i < X && base[i < X ? i : 0] <= q)) - 1;
-    const int b0 = uniform(base[x]), mts = uniform(base[x + 1]) - b0;
+    const int x = c * 16 + __popcll(ballot(lane < 16 && i < X && E.base[i < X ? i : 0] <= q)) - 1;
+    const int b0 = uniform(E.base[x]), mts = uniform(E.base[x + 1]) - b0;
     // row tiles in groups: within a group every row tile meets a weight tile before the next one
     // comes, so that both stay in the XCD's cache while its CUs use them
     const int in = t - b0 * ntn, g = in / (kGroupTiles * ntn), r = in - g * kGroupTiles * ntn;
     const int left = mts - g * kGroupTiles, gm = left < kGroupTiles ? left : kGroupTiles;
     Place p;
-    int first;
-    p.cnt = uniform(expert_rows(P, x, &first));
+    p.cnt = uniform(E.rows[x]);
     // the expert's tiles share its rows evenly, in parts of 16
     const int rows = ((p.cnt + mts - 1) / mts + 15) & ~15;
     p.m0 = (g * kGroupTiles + r % gm) * rows;
@@ -137,173 +154,120 @@ __device__ __forceinline__ Place place_of(const Product& P, const int* base, int
     p.end = p.m0 + rows < p.cnt ? p.m0 + rows : p.cnt;
     const int d = P.rb + x / P.L;
     p.e = (long)d * P.L + x % P.L;
-    p.row0 = (long)d * P.B + uniform(first);
+    p.row0 = (long)d * P.B + uniform(E.first[x]);
     return p;
 }
 
-// Where a wave loads a stage of a tile from: the tile's first row, weight row and (gated) up row, an
-// offset of the lane for each fill, and the lane's scale.
-template <class T>
-struct Source {
-    const uint8_t *rows, *weights, *ups;
-    uint32_t off[T::kPerWave];
-    const float* scale;
-};
-
-// Fill i = wave + 8 j of a stage brings rows 8 (i % kFillsPerStep) .. + 7 of step i / kFillsPerStep.
-template <class T>
-struct Fill {
-    int kp, r;  // step; first of its rows: BM rows, then BN weight rows
-    __device__ __forceinline__ Fill(int wave, int j) {
-        const int i = (wave & 7) + j * kWaves;
-        kp = T::KP == 1 ? 0 : i / T::kFillsPerStep;
-        r = (i - kp * T::kFillsPerStep) * 8;
-    }
-    template <bool GATED>
-    __device__ __forceinline__ const uint8_t* of(const uint8_t* rows, const uint8_t* weights, const uint8_t* ups) const {
-        return r < T::BM ? rows : GATED && (r - T::BM & 16) ? ups : weights;
-    }
-};
-
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 16, 0, 0);
+__device__ __forceinline__ void load_lds16(const void* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
 }
-__device__ __forceinline__ void load_lds4(const float* src, float* dst) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (lds_void*)dst, 4, 0, 0);
+__device__ __forceinline__ void load_lds4(const void* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 4, 0, 0);
 }
 
-// Lane l of a fill lands at row l / 8, place l % 8, and fetches the row's 16-byte chunk (l % 8) ^ (l / 8):
-// the reads of a 16-row part then spread over the LDS banks.  Rows past an expert's last repeat it;
-// weight rows past the last repeat it too.  For the gated product the weight rows of a tile alternate,
-// 16 gate rows and 16 up rows.
+// A wave's loads of rows or of weights, stage after stage, tile after tile.  Lane l of a fill (8 rows of
+// a step) lands at row l / 8, place l % 8, and fetches the row's 16-byte chunk (l % 8) ^ (l / 8): the reads
+// of a 16-row part then spread over the LDS banks.  Rows past an expert's last repeat it; weight rows
+// past the last repeat it too.  For the gated product the weight rows of a tile alternate, 16 gate rows
+// and 16 up rows.
 template <bool FP8, bool GATED, class T>
-__device__ __forceinline__ void aim(const Product& P, const Place& p, Source<T>& s) {
-    const int lane = lane_id(), wave = uniform(wave_id());
-    const int wrows = GATED ? 2 * P.C : P.C;
-    const int chunk = (lane & 7) ^ (lane >> 3), r8 = lane >> 3;
-    s.rows = P.a + (p.row0 + p.m0) * P.KB;
-    s.weights = P.w + (p.e * wrows + p.n0) * P.KB;
-    s.ups = s.weights + (long)P.C * P.KB;
-#pragma unroll
-    for (int j = 0; j < T::kPerWave; ++j) {
-        const Fill<T> f(wave, j);
-        const int q = f.r - T::BM;
-        const bool tok = q < 0;
-        const int r = (tok ? f.r : GATED ? (q >> 5) * 16 + (q & 15) : q) + r8;
-        const int last = tok ? p.cnt - 1 - p.m0 : P.C - 1 - p.n0;
-        s.off[j] = (uint32_t)(r < last ? r : last) * P.KB + f.kp * kStepBytes + chunk * 16;
-    }
-    if constexpr (FP8) {
-        const int i = threadIdx.x, kp = i / (T::BM + 2), r = i - kp * (T::BM + 2);
-        const int blocks = (wrows + 127) / 128;
-        if (r < T::BM || kp >= T::KP) {
-            const int m = p.m0 + r < p.cnt ? p.m0 + r : p.cnt - 1;
-            s.scale = P.as + (p.row0 + m) * P.KS + (kp < T::KP ? kp : 0);
+struct Loader {
+    const uint8_t *from, *ups;  // the tile's first row, or its first weight row and up row
+    uint32_t off[T::F];         // the lane's offset for each fill
+    const float* scale[2];      // the lane's scales (e4m3, waves that load rows)
+    int tile, k;                // next to load: stage k of a tile
+    int slot, group;
+
+    // Fill j of the wave's: fill i of the stage, its step and its first row.
+    __device__ __forceinline__ static int fill(int j, bool rows) { return (uniform(wave_id()) & 3) * (rows ? T::FR : T::FW) + j; }
+
+    __device__ __forceinline__ void aim(const Product& P, const Experts& E, int X, int ntn, bool rows) {
+        const Place p = place_of<T, GATED>(P, E, X, ntn, tile);
+        const int lane = lane_id();
+        const int wrows = GATED ? 2 * P.C : P.C;
+        const int chunk = (lane & 7) ^ (lane >> 3), r8 = lane >> 3;
+        if (rows) {
+            from = ups = P.a + (p.row0 + p.m0) * P.KB;
         } else {
-            int b = GATED ? (p.n0 + (r - T::BM) * P.C) / 128 : p.n0 / 128 + (r - T::BM);
-            b = b < blocks ? b : blocks - 1;
-            s.scale = P.ws + (p.e * blocks + b) * P.KS + kp;
+            from = P.w + (p.e * wrows + p.n0) * P.KB;
+            ups = from + (long)P.C * P.KB;
         }
-    }
-}
-
-// Loads stage k of the tile that `src` aims at into `wr`.
-template <bool FP8, bool GATED, class T>
-__device__ __forceinline__ void fetch_stage(uint8_t* wr, const Product& P, const Source<T>& src, int k) {
-    const int lane = lane_id(), wave = uniform(wave_id());
-    const int kb = k * T::KP * kStepBytes;
-    const uint8_t *rows = src.rows + kb, *weights = src.weights + kb, *ups = src.ups + kb;
-    if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) {
+        const int last = rows ? p.cnt - 1 - p.m0 : P.C - 1 - p.n0;
 #pragma unroll
-        for (int j = 0; j < T::kPerWave; ++j) {
-            const Fill<T> f(wave, j);
-            if (T::kFills % kWaves == 0 || wave + j * kWaves < T::kFills)
-                load_lds16(f.template of<GATED>(rows, weights, ups) + src.off[j], wr + (wave + j * kWaves) * 1024);
+        for (int j = 0; j < T::F; ++j) {
+            const int i = fill(j, rows), per = (rows ? T::BM : T::BN) / 8;
+            const int kp = i / per, q = (i - kp * per) * 8;
+            const int r = (!rows && GATED ? (q >> 5) * 16 + (q & 15) : q) + r8;
+            off[j] = (uint32_t)(r < last ? r : last) * P.KB + kp * kStepBytes + chunk * 16;
         }
-    } else {  // the last stage of a row: zeros from the row's end on
-        const int chunk = (lane & 7) ^ (lane >> 3);
+        if constexpr (FP8) {
+            if (rows) {
+                const int blocks = (wrows + 127) / 128;
 #pragma unroll
-        for (int j = 0; j < T::kPerWave; ++j) {
-            const Fill<T> f(wave, j);
-            uint32_t off = src.off[j];
-            asm volatile("" : "+v"(off));  // keeps this path's addresses out of the other's registers
-            const bool in = kb + f.kp * kStepBytes + chunk * 16 < P.KB;
-            if (T::kFills % kWaves == 0 || wave + j * kWaves < T::kFills)
-                load_lds16(in ? f.template of<GATED>(rows, weights, ups) + off : kZeros, wr + (wave + j * kWaves) * 1024);
-        }
-    }
-    if constexpr (FP8) {
-        // a step past the last reads the row's last scale (its codes are zeros)
-        const int kp = threadIdx.x / (T::BM + 2);
-        const int ks = k * T::KP, over = ks + (kp < T::KP ? kp : 0) - (P.KS - 1);
-        load_lds4(src.scale + ks - (over > 0 ? over : 0), (float*)(wr + T::kTileBytes) + wave * 64);
-    }
-}
-
-// One stage: the loads of stage k of a tile into `wr` (if `fetch`), and the products of the stage in
-// `rd`.  The two never overlap; saying so (__restrict__ on both) keeps the compiler from making the
-// reads wait for the loads.
-template <bool FP8, bool GATED, class T>
-__device__ __forceinline__ void stage_step(const uint8_t* __restrict__ rd, uint8_t* __restrict__ wr, const Product& P,
-                                           const Source<T>& src, int k, bool fetch, f32x4 (&acc)[T::NT][T::MT]) {
-    constexpr int MT = T::MT, NT = T::NT;
-    const int lane = lane_id(), wave = uniform(wave_id());
-    if (fetch) fetch_stage<FP8, GATED, T>(wr, P, src, k);
-    const int r16 = lane & 15, g = lane >> 4;
-    const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
-    float sr[MT], sw[2];
-    if constexpr (FP8) {
-        const float* scl = (const float*)(rd + T::kTileBytes) + kp * (T::BM + 2);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) sr[j] = scl[(j * T::WM + wm) * 16 + r16];
-        sw[0] = scl[T::BM + (GATED ? 0 : wn * NT * 16 / 128)];
-        sw[1] = GATED ? scl[T::BM + 1] : sw[0];
-    }
-    // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
-    const int p0 = (g ^ (r16 & 7)) * 16, p1 = p0 ^ 64;
-    const uint8_t* ta = rd + (kp * (T::BM + T::BN) + wm * 16 + r16) * kStepBytes;
-    constexpr int kNext = T::WM * 16 * kStepBytes;  // to the wave's next part
-    const uint8_t* tw = rd + (kp * (T::BM + T::BN) + T::BM + wn * NT * 16 + r16) * kStepBytes;
-    i32x4 w[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        w[i][0] = *(const i32x4*)(tw + i * 16 * kStepBytes + p0);
-        w[i][1] = *(const i32x4*)(tw + i * 16 * kStepBytes + p1);
-    }
-    i32x4 b[2][2];
-    b[0][0] = *(const i32x4*)(ta + p0);
-    b[0][1] = *(const i32x4*)(ta + p1);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        // the next part's rows are read while this one's products run; no further ahead, for the
-        // registers' sake
-        if (j + 1 < MT) {
-            b[(j + 1) & 1][0] = *(const i32x4*)(ta + (j + 1) * kNext + p0);
-            b[(j + 1) & 1][1] = *(const i32x4*)(ta + (j + 1) * kNext + p1);
-        }
-        const i32x4 b0 = b[j & 1][0], b1 = b[j & 1][1];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            if constexpr (FP8) {
-                const i32x8 A = __builtin_shufflevector(w[i][0], w[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-                const f32x4 p =
-                    __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-                const float s = sr[j] * sw[GATED ? (i & 1) : 0];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], s, acc[i][j][v]);
-                // here, and not after all products: the partial sums would need registers of their own
-                asm volatile("" : "+v"(acc[i][j]));
-            } else {
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, w[i][0]), __builtin_bit_cast(bf16x8, b0), acc[i][j], 0, 0, 0);
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, w[i][1]), __builtin_bit_cast(bf16x8, b1), acc[i][j], 0, 0, 0);
+                for (int u = 0; u < 2; ++u) {
+                    const int r = (uniform(wave_id()) + u * 4) * kWave + lane, j = r - T::BM;
+                    const int m = r < last ? r : last;
+                    int b = GATED ? (p.n0 + (j & 1) * P.C) / 128 : p.n0 / 128 + (j & 1);
+                    b = b < blocks ? b : blocks - 1;
+                    scale[u] = j < 0 || j > 1 ? P.as + (p.row0 + p.m0 + m) * P.KS : P.ws + (p.e * blocks + b) * P.KS;
+                }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
     }
-}
+
+    // Loads the next stage into the ring and moves on.
+    __device__ __forceinline__ void load(const Product& P, const Experts& E, int X, int ntn, int tiles, int G, int stages,
+                                         uint8_t* ring, bool rows) {
+        const int lane = lane_id();
+        const int kb = k * T::KP * kStepBytes;
+        uint8_t* to = ring + (rows ? slot * T::kRowSlot : T::kWeightsAt + slot * T::kWeightSlot) + fill(0, rows) * 1024;
+        if constexpr (FP8) {
+            const int ks = k * T::KP;
+            if (rows && ks % 4 == 0) {
+                uint8_t* st = ring + T::kScalesAt + group * T::kScaleSlot;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int w = uniform(wave_id()) + u * 4;
+                    if (u * 4 >= T::kScaleLoads || w >= T::kScaleLoads) break;
+                    if (P.KS % 4 == 0) {  // 16-byte rows of scales
+                        load_lds16(scale[u] + ks, st + w * 1024);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            load_lds4(scale[u] + (ks + q < P.KS ? ks + q : P.KS - 1), st + (q * T::kScaleLoads + w) * 256);
+                    }
+                }
+                group = group == T::SR - 1 ? 0 : group + 1;
+            }
+        }
+        const uint8_t *f = from + kb, *v = ups + kb;
+        const int mine = rows ? T::FR : T::FW, per = (rows ? T::BM : T::BN) / 8;
+        if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) {
+#pragma unroll
+            for (int j = 0; j < T::F; ++j) {
+                const bool up = GATED && (fill(j, rows) % per) & 2;
+                if (T::FR == T::FW || j < mine) load_lds16((up ? v : f) + off[j], to + j * 1024);
+            }
+        } else {  // the last stage of a row: zeros from the row's end on
+            const int chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+            for (int j = 0; j < T::F; ++j) {
+                const int i = fill(j, rows);
+                const bool up = GATED && (i % per) & 2;
+                uint32_t o = off[j];
+                asm volatile("" : "+v"(o));  // keeps this path's addresses out of the other's registers
+                const bool in = kb + i / per * kStepBytes + chunk * 16 < P.KB;
+                if (T::FR == T::FW || j < mine) load_lds16(in ? (up ? v : f) + o : kZeros, to + j * 1024);
+            }
+        }
+        slot = slot == (rows ? T::SR : T::SW) - 1 ? 0 : slot + 1;
+        if (++k == stages) {
+            k = 0;
+            tile += G;
+            if (tile < tiles) aim(P, E, X, ntn, rows);
+        }
+    }
+};
 
 // A tile's results: the lane's row of each 16-row part, four neighbouring columns of each 16-column
 // part.  `epi`: LDS apart from the ring.
@@ -404,66 +368,123 @@ __device__ __forceinline__ void write_tile(const Product& P, const Place& p, f32
     }
 }
 
-// The block's tiles, v, v + G, ..., as one run of stages: the loads run S - 1 stages ahead of the
-// products, across the ends of tiles.
+// The block's tiles, v, v + G, ..., as one run of stages: the loads run ahead of the products, across
+// the ends of tiles.
 template <bool FP8, bool GATED, class T>
-__device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const int* base, float* epi, int X, int v,
+__device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const Experts& E, float* epi, int X, int v,
                                           int G) {
-    constexpr int kStage = T::template stage<FP8>(), S = T::S;
-    static_assert(S * kStage <= kRingBytes, "the ring");
-    constexpr int kLoads = T::kPerWave + (FP8 ? 1 : 0);  // of a stage, at most
-    // waves with fewer fills than others wait for one stage more than they need
-    constexpr int kFew = T::kFills / kWaves + (FP8 ? 1 : 0);
+    static_assert(T::template bytes<FP8>() <= kRingBytes, "the ring");
+    constexpr int MT = T::MT, NT = T::NT;
     const int ntn = (P.C + (GATED ? T::BN / 2 : T::BN) - 1) / (GATED ? T::BN / 2 : T::BN);
-    const int tiles = base[X] * ntn;
+    const int tiles = E.base[X] * ntn;
     if (v >= tiles) return;
     const int stages = (P.KB + T::KP * kStepBytes - 1) / (T::KP * kStepBytes);
     const long total = (long)((tiles - 1 - v) / G + 1) * stages;
-    const bool many = uniform(wave_id()) < T::kFills % kWaves;
-    f32x4 acc[T::NT][T::MT];
-    Source<T> src;
-    Place p = place_of<T, GATED>(P, base, X, ntn, v);
-    aim<FP8, GATED, T>(P, p, src);
-    int lt = v, lk = 0, ct = v, ck = 0;  // tile and stage of the loads and of the products
-    int rslot = 0, wslot = 0;
+    const int lane = lane_id(), wave = uniform(wave_id());
+    const bool rows = wave < T::WR, weights = wave >= kWaves - T::WW;
+    const int lead = rows ? T::kRowLead : T::kWeightLead;
+    Loader<FP8, GATED, T> L;
+    L.tile = v;
+    L.k = L.slot = L.group = 0;
+    if (rows || weights) {
+        L.aim(P, E, X, ntn, rows);
+        for (int n = 0; n < lead && n < total; ++n) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
+    }
+    f32x4 acc[NT][MT];
     auto zero = [&] {
 #pragma unroll
-        for (int i = 0; i < T::NT; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < T::MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     };
     zero();
-    auto advance = [&] {
-        ++lk;
-        wslot = wslot == S - 1 ? 0 : wslot + 1;
-        if (lk == stages) {
-            lk = 0;
-            lt += G;
-            if (lt < tiles) aim<FP8, GATED, T>(P, place_of<T, GATED>(P, base, X, ntn, lt), src);
-        }
-    };
-    for (int n = 0; n < S - 1 && n < total; ++n) {
-        fetch_stage<FP8, GATED, T>(ring + wslot * kStage, P, src, lk);
-        advance();
-    }
+    const int r16 = lane & 15, g = lane >> 4;
+    const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
+    // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
+    const int p0 = (g ^ (r16 & 7)) * 16, p1 = p0 ^ 64;
+    const int at_a = (kp * T::BM + wm * 16 + r16) * kStepBytes;
+    const int at_w = T::kWeightsAt + (kp * T::BN + wn * NT * 16 + r16) * kStepBytes;
+    constexpr int kNext = T::WM * 16 * kStepBytes;  // to the wave's next 16 rows
+    Place p = place_of<T, GATED>(P, E, X, ntn, v);
+    int ct = v, ck = 0, rslot = 0, wslot = 0, group = -1;
     for (long n = 0; n < total; ++n) {
-        if (n + S - 1 <= total) {
-            if (T::kFills % kWaves && many) wait_loads<(S - 2) * kLoads>();
-            else wait_loads<(S - 2) * (T::kFills % kWaves ? kFew : kLoads)>();
-        } else {
-            wait_loads<0>();
+        if (rows) {
+            if (n + T::kRowLead <= total) wait_loads<(T::kRowLead - 1) * T::FR>();
+            else wait_loads<0>();
+        } else if (weights) {
+            if (n + T::kWeightLead <= total) wait_loads<(T::kWeightLead - 1) * T::FW>();
+            else wait_loads<0>();
         }
         lds_barrier();
-        const bool fetch = n + S - 1 < total;
-        stage_step<FP8, GATED, T>(ring + rslot * kStage, ring + wslot * kStage, P, src, lk, fetch, acc);
-        rslot = rslot == S - 1 ? 0 : rslot + 1;
-        if (fetch) advance();
+        const bool more = n + lead < total;
+        if (more && (rows || (weights && !T::EARLY))) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
+        const uint8_t* ta = ring + rslot * T::kRowSlot + at_a;
+        const uint8_t* tw = ring + wslot * T::kWeightSlot + at_w;
+        float sr[MT], sw[2];
+        if constexpr (FP8) {
+            const int ks = ck * T::KP;
+            if (ks % 4 == 0) group = group == T::SR - 1 ? 0 : group + 1;
+            // 16 bytes a row, or the four steps apart
+            const bool by_row = P.KS % 4 == 0;
+            const int one = by_row ? 4 : 1;
+            const float* sc = (const float*)(ring + T::kScalesAt + group * T::kScaleSlot) +
+                              (ks + kp) % 4 * (by_row ? 1 : T::kScaleLoads * kWave);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) sr[j] = sc[((j * T::WM + wm) * 16 + r16) * one];
+            sw[0] = sc[(T::BM + (GATED ? 0 : wn * NT * 16 / 128)) * one];
+            sw[1] = GATED ? sc[(T::BM + 1) * one] : sw[0];
+        }
+        i32x4 w[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            w[i][0] = *(const i32x4*)(tw + i * 16 * kStepBytes + p0);
+            w[i][1] = *(const i32x4*)(tw + i * 16 * kStepBytes + p1);
+        }
+        i32x4 b[2][2];
+        b[0][0] = *(const i32x4*)(ta + p0);
+        b[0][1] = *(const i32x4*)(ta + p1);
+        if constexpr (T::EARLY) {
+            lds_barrier();  // every wave has its weights
+            if (more && weights) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            // the next part's rows are read while this one's products run; no further ahead, for the
+            // registers' sake
+            if (j + 1 < MT) {
+                b[(j + 1) & 1][0] = *(const i32x4*)(ta + (j + 1) * kNext + p0);
+                b[(j + 1) & 1][1] = *(const i32x4*)(ta + (j + 1) * kNext + p1);
+            }
+            const i32x4 b0 = b[j & 1][0], b1 = b[j & 1][1];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if constexpr (FP8) {
+                    const i32x8 A = __builtin_shufflevector(w[i][0], w[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    const f32x4 q =
+                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                    const float s = sr[j] * sw[GATED ? (i & 1) : 0];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[i][j][u] = __builtin_fmaf(q[u], s, acc[i][j][u]);
+                    // here, and not after all products: the partial sums would need registers of their own
+                    asm volatile("" : "+v"(acc[i][j]));
+                } else {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, w[i][0]), __builtin_bit_cast(bf16x8, b0), acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, w[i][1]), __builtin_bit_cast(bf16x8, b1), acc[i][j], 0, 0, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        rslot = rslot == T::SR - 1 ? 0 : rslot + 1;
+        wslot = wslot == T::SW - 1 ? 0 : wslot + 1;
         if (++ck == stages) {
             write_tile<FP8, GATED, T>(P, p, acc, epi);
             zero();
             ck = 0;
             ct += G;
-            if (ct < tiles) p = place_of<T, GATED>(P, base, X, ntn, ct);
+            if (ct < tiles) p = place_of<T, GATED>(P, E, X, ntn, ct);
         }
     }
     lds_barrier();
@@ -472,38 +493,34 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
 // The tiles, from few rows and columns to many.  The gated product needs two 16-row parts of a tile's
 // weight rows in each wave (gate and up), and with e4m3 operands 256 of them in a tile: it quantises
 // blocks of 128 output columns.
-constexpr int kTiles = 11, kLevels = 5;
+constexpr int kLevels = 4;
 enum { kPlain, kGated, kWide };
 template <int KIND, int I> struct TileOf;
-template <> struct TileOf<kPlain, 0> { typedef Tile<16, 32, 1, 2, 4, 5> type; };
-template <> struct TileOf<kPlain, 1> { typedef Tile<32, 32, 2, 2, 2, 8> type; };
-template <> struct TileOf<kPlain, 2> { typedef Tile<16, 64, 1, 4, 2, 6> type; };
-template <> struct TileOf<kPlain, 3> { typedef Tile<64, 64, 2, 4, 1, 8> type; };
-template <> struct TileOf<kPlain, 4> { typedef Tile<16, 128, 1, 8, 1, 7> type; };
-template <> struct TileOf<kPlain, 5> { typedef Tile<32, 128, 1, 8, 1, 6> type; };
-template <> struct TileOf<kPlain, 6> { typedef Tile<64, 128, 2, 4, 1, 5> type; };
-template <> struct TileOf<kGated, 0> { typedef Tile<16, 32, 1, 1, 8, 3> type; };
-template <> struct TileOf<kGated, 1> { typedef Tile<32, 32, 2, 1, 4, 4> type; };
-template <> struct TileOf<kGated, 2> { typedef Tile<16, 64, 1, 2, 4, 3> type; };
-template <> struct TileOf<kGated, 3> { typedef Tile<64, 64, 4, 2, 1, 8> type; };
-template <> struct TileOf<kGated, 4> { typedef Tile<16, 128, 1, 4, 2, 4> type; };
-template <> struct TileOf<kGated, 5> { typedef Tile<32, 128, 2, 4, 1, 7> type; };
-template <> struct TileOf<kGated, 6> { typedef Tile<64, 128, 2, 4, 1, 6> type; };
-template <> struct TileOf<kWide, 4> { typedef Tile<16, 256, 1, 8, 1, 4> type; };
-template <> struct TileOf<kWide, 5> { typedef Tile<32, 256, 1, 8, 1, 3> type; };
-template <> struct TileOf<kWide, 6> { typedef Tile<64, 256, 1, 8, 1, 3> type; };
-template <> struct TileOf<kWide, 7> { typedef Tile<128, 256, 2, 4, 1, 3> type; };
-template <int KIND> struct TileOf<KIND, 7> { typedef Tile<128, 128, 2, 4, 1, 4> type; };
-template <int KIND> struct TileOf<KIND, 8> { typedef Tile<160, 256, 2, 4, 1, 2> type; };
-template <int KIND> struct TileOf<KIND, 9> { typedef Tile<192, 256, 2, 4, 1, 2> type; };
-template <int KIND> struct TileOf<KIND, 10> { typedef Tile<256, 256, 2, 4, 1, 2> type; };
+template <> struct TileOf<kPlain, 0> { typedef Tile<16, 32, 1, 2, 4, 3, 7> type; };
+template <> struct TileOf<kPlain, 1> { typedef Tile<32, 32, 1, 2, 4, 3, 5> type; };
+template <> struct TileOf<kPlain, 2> { typedef Tile<16, 64, 1, 4, 2, 4, 7> type; };
+template <> struct TileOf<kPlain, 3> { typedef Tile<32, 64, 1, 4, 2, 3, 7> type; };
+template <> struct TileOf<kGated, 0> { typedef Tile<16, 32, 1, 1, 8, 2, 3> type; };
+template <> struct TileOf<kGated, 1> { typedef Tile<32, 32, 2, 1, 4, 3, 5> type; };
+template <> struct TileOf<kGated, 2> { typedef Tile<16, 64, 1, 2, 4, 3, 3> type; };
+template <> struct TileOf<kGated, 3> { typedef Tile<32, 64, 2, 2, 2, 3, 7> type; };
+template <int KIND> struct TileOf<KIND, 4> { typedef Tile<64, 64, 2, 2, 2, 3, 5> type; };
+template <int KIND> struct TileOf<KIND, 5> { typedef Tile<64, 128, 2, 4, 1, 3, 7> type; };
+template <int KIND> struct TileOf<KIND, 6> { typedef Tile<128, 128, 2, 4, 1, 3, 5> type; };
+template <> struct TileOf<kWide, 3> { typedef Tile<16, 256, 1, 8, 1, 4, 4> type; };
+template <> struct TileOf<kWide, 4> { typedef Tile<32, 256, 1, 8, 1, 3, 4> type; };
+template <> struct TileOf<kWide, 5> { typedef Tile<64, 256, 1, 8, 1, 3, 3> type; };
+template <int KIND> struct TileOf<KIND, 7> { typedef Tile<128, 256, 2, 4, 1, 2, 3> type; };
+template <int KIND> struct TileOf<KIND, 8> { typedef Tile<160, 256, 2, 4, 1, 2, 2, true> type; };
+template <int KIND> struct TileOf<KIND, 9> { typedef Tile<192, 256, 2, 4, 1, 2, 2, true> type; };
+template <int KIND> struct TileOf<KIND, 10> { typedef Tile<256, 256, 2, 4, 1, 2, 2, true> type; };
 
 // At each level an expert's rows make as few row tiles as fit `most` rows each (0: the largest tile;
 // further levels smaller ones, for products that would leave CUs without a tile), and the tiles take
 // the least height that holds their even share.
 template <bool WIDE>
 __device__ __forceinline__ int level_rows(int level) {
-    return level == 0 ? 256 : level == 1 ? 128 : WIDE || level <= 3 ? 64 : 32;
+    return level == 0 ? 256 : level == 1 ? 128 : WIDE || level == 2 ? 64 : 32;
 }
 template <bool WIDE>
 __device__ __forceinline__ int row_tiles(int rows, int level) {
@@ -512,21 +529,22 @@ __device__ __forceinline__ int row_tiles(int rows, int level) {
 template <bool WIDE>
 __device__ __forceinline__ int tile_of(int rows, int level) {
     const int mts = row_tiles<WIDE>(rows, level), n = (rows + mts - 1) / (mts > 0 ? mts : 1);
-    if (!WIDE && level == 4) return n > 16 ? 1 : 0;
-    if (!WIDE && level == 3) return n > 16 ? 3 : 2;
-    return n > 192 ? 10 : n > 160 ? 9 : n > 128 ? 8 : n > 64 ? 7 : n > 32 ? 6 : n > 16 ? 5 : 4;
+    if (WIDE) return n > 192 ? 10 : n > 160 ? 9 : n > 128 ? 8 : n > 64 ? 7 : n > 32 ? 5 : n > 16 ? 4 : 3;
+    if (level == 3) return n > 16 ? 1 : 0;
+    if (n <= 32) return n > 16 ? 3 : 2;
+    if (level == 2) return 4;
+    if (n <= 64) return 5;
+    return level == 1 ? 6 : n > 192 ? 10 : n > 160 ? 9 : n > 128 ? 8 : 7;
 }
 
 // Columns of weight rows of a tile, and the time of a step over K, in cycles.
 template <bool WIDE>
 __device__ __forceinline__ int tile_width(int i) {
-    return WIDE || i >= 8 ? 256 : i >= 4 ? 128 : i >= 2 ? 64 : 32;
+    return WIDE || i >= 7 ? 256 : i >= 5 ? 128 : i >= 2 ? 64 : 32;
 }
 template <bool WIDE>
 __device__ __forceinline__ int tile_time(int i, int rows) {
-    if (i >= 8) return 1000 + 8 * rows;
-    if (WIDE) return 700 + 8 * rows;
-    return i >= 4 ? 450 + 4 * rows : i >= 2 ? 300 + 2 * rows : 200 + rows;
+    return tile_width<WIDE>(i) * 4 + rows * tile_width<WIDE>(i) / 32 + 150;
 }
 
 // base[x] = row tiles of tile i of the experts before x.
@@ -561,7 +579,7 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
     constexpr int KIND = WIDE ? kWide : GATED ? kGated : kPlain;
     __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes];
     __shared__ __attribute__((aligned(16))) float epi[kEpiBytes / 4];
-    __shared__ int base[kMaxExperts + 1];
+    __shared__ Experts E;
     __shared__ int part[kWaves];
     __shared__ unsigned long long sum[kLevels];
     __shared__ int most[kLevels];
@@ -580,8 +598,10 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int x = 2 * threadIdx.x + i;
-        int first;
-        if (x < X) rows[i] = expert_rows(P, x, &first);
+        if (x < X) {
+            rows[i] = expert_rows(P, x, &E.first[x]);
+            E.rows[x] = rows[i];
+        }
     }
     // the level whose tiles end first: their times over all blocks, or the longest of them
     constexpr int levels = WIDE ? 3 : kLevels;
@@ -627,22 +647,22 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
     auto run = [&](auto tile, int i) {
         typedef decltype(tile) T;
         if (!(all >> i & 1)) return;
-        scan_tiles<WIDE>(rows, level, i, X, base, part);
+        scan_tiles<WIDE>(rows, level, i, X, E.base, part);
         int w = v - done % G;
         w = w < 0 ? w + G : w;
-        run_tiles<FP8, GATED, T>(P, ring, base, epi, X, w, G);
+        run_tiles<FP8, GATED, T>(P, ring, E, epi, X, w, G);
         const int cols = GATED ? T::BN / 2 : T::BN;
-        done += uniform(base[X]) * ((P.C + cols - 1) / cols);
+        done += uniform(E.base[X]) * ((P.C + cols - 1) / cols);
     };
     run(typename TileOf<KIND, 10>::type(), 10);
     run(typename TileOf<KIND, 9>::type(), 9);
     run(typename TileOf<KIND, 8>::type(), 8);
     run(typename TileOf<KIND, 7>::type(), 7);
-    run(typename TileOf<KIND, 6>::type(), 6);
+    if constexpr (!WIDE) run(typename TileOf<KIND, 6>::type(), 6);
     run(typename TileOf<KIND, 5>::type(), 5);
     run(typename TileOf<KIND, 4>::type(), 4);
+    run(typename TileOf<KIND, 3>::type(), 3);
     if constexpr (!WIDE) {
-        run(typename TileOf<KIND, 3>::type(), 3);
         run(typename TileOf<KIND, 2>::type(), 2);
         run(typename TileOf<KIND, 1>::type(), 1);
         run(typename TileOf<KIND, 0>::type(), 0);
