@@ -5,6 +5,8 @@
 //             v[q][c] = sum_b as[q][b] ws[e][c/128][b] p_b[q][c]       e4m3: p_b the fp32 sum over the
 //                                                                      128 values k of block b
 //   gated     h = g / (1 + exp(-g)) * u,  g = v[q][c], u = v[q][I + c]
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -29,6 +31,7 @@ struct Product {
     int KB, KS;   // bytes of a row; scales of a row (e4m3)
     int C;
     int L, rb, rc;
+    int ntn[4];   // tiles side by side over the C columns, for tiles of 32, 64, 128 and 256 weight rows
 };
 
 constexpr int kStepBytes = 128;    // of every row, per step over K: 64 bf16 or 128 e4m3 values
@@ -45,30 +48,36 @@ __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
 // The shape of a tile: BM rows x BN weight rows by WM x WN x KP waves (KP: waves that share a
 // tile's part and take every KP-th step).  A stage is KP steps.  The rows go through a ring of SR
-// stages, loaded by the first waves, the weights through one of SW, loaded by the last four: a wave
-// waits for its loads in their order, so rows (short way, from the cache) and weights (long way, from
-// memory) wait apart.  EARLY: a stage's weights are read into registers at its begin and their place
-// refilled at once, not after the stage.
-template <int BM_, int BN_, int WM_, int WN_, int KP_, int SR_, int SW_, bool EARLY_ = false>
+// stages, the weights through one of SW.  Small tiles: the first waves load the rows and the last four
+// the weights; a wave waits for its loads in their order, so rows (short way, from the cache) and
+// weights (long way, from memory) wait apart.  EARLY: a stage is read into registers whole and its
+// place refilled before its products, which leaves one stage more in flight.  AHEAD (tiles bound by
+// arithmetic): every wave loads its share of both between its products; a stage's weights are read
+// into registers during the stage before, and their place in the ring is refilled from the middle of
+// the stage on.
+enum { kRing, kEarly, kAhead };
+template <int BM_, int BN_, int WM_, int WN_, int KP_, int SR_, int SW_, int MODE = kRing>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KP = KP_, SR = SR_, SW = SW_;
-    static constexpr bool EARLY = EARLY_;
+    static constexpr bool AHEAD = MODE == kAhead, EARLY = MODE == kEarly;
+    static_assert(!AHEAD || (SR == 2 && SW == 2 && KP == 1), "two stages");
     static_assert(WM * WN * KP == kWaves, "eight waves");
     static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 parts of a wave
-    // waves that load rows and weights, and the loads of 8 rows of each, a stage
+    // waves that load rows and weights, and the loads of 8 rows that each makes, a stage
     static constexpr int kRowFills = KP * BM / 8, kWeightFills = KP * BN / 8;
-    static constexpr int WR = kRowFills < 4 ? kRowFills : 4, WW = 4;
-    static constexpr int FR = kRowFills / WR, FW = kWeightFills / WW, F = FR > FW ? FR : FW;
+    static constexpr int WR = AHEAD ? kWaves : kRowFills < 4 ? kRowFills : 4, WW = AHEAD ? kWaves : 4;
+    static constexpr int FR = kRowFills / WR, FW = kWeightFills / WW;
     static_assert(FR * WR == kRowFills && FW * WW == kWeightFills, "whole fills");
     // stages that the loads run ahead
-    static constexpr int kRowLead = SR - 1, kWeightLead = EARLY ? SW : SW - 1;
+    static constexpr int kRowLead = EARLY ? SR : SR - 1, kWeightLead = AHEAD || EARLY ? SW : SW - 1;
     static constexpr int kRowSlot = KP * BM * kStepBytes, kWeightSlot = KP * BN * kStepBytes;
     // e4m3: the scales of four steps, 16 bytes for each row and for the tile's two weight blocks
     static constexpr int kScaleLoads = (BM + 2 + kWave - 1) / kWave, kScaleSlot = kScaleLoads * kWave * 16;
+    static constexpr int kScaleSlots = EARLY ? SR + 1 : SR;
     static_assert(4 % KP == 0 || KP == 8, "whole stages of scales");
     static constexpr int kWeightsAt = SR * kRowSlot, kScalesAt = kWeightsAt + SW * kWeightSlot;
     template <bool FP8>
-    static constexpr int bytes() { return kScalesAt + (FP8 ? SR * kScaleSlot : 0); }
+    static constexpr int bytes() { return kScalesAt + (FP8 ? kScaleSlots * kScaleSlot : 0); }
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -125,44 +134,67 @@ struct Place {
     long e;
 };
 
-// Of each expert of the call, in LDS: row tiles before it, first row, rows.
+// Of each expert of the call, in LDS: tiles before it, first row, rows.
 struct Experts {
     int base[kMaxExperts + 1];
     int first[kMaxExperts];
     int rows[kMaxExperts];
 };
 
+// What the loads and the products of a block's tiles go by.
+struct Run {
+    uint32_t ring;  // its LDS address
+    int X, ntn, tiles, G, stages;
+};
+
 template <class T, bool GATED>
-__device__ __forceinline__ Place place_of(const Product& P, const Experts& E, int X, int ntn, int t) {
-    // the last expert with base[x] <= q: 16 at a time, then one by one
-    const int q = t / ntn, lane = lane_id();
-    int i = lane * 16;
-    const int c = __popcll(ballot(i < X && E.base[i < X ? i : 0] <= q)) - 1;
-    i = c * 16 + lane;
-    const int x = c * 16 + __popcll(ballot(lane < 16 && i < X && E.base[i < X ? i : 0] <= q)) - 1;
-    const int b0 = uniform(E.base[x]), mts = uniform(E.base[x + 1]) - b0;
-    // row tiles in groups: within a group every row tile meets a weight tile before the next one
-    // comes, so that both stay in the XCD's cache while its CUs use them
-    const int in = t - b0 * ntn, g = in / (kGroupTiles * ntn), r = in - g * kGroupTiles * ntn;
-    const int left = mts - g * kGroupTiles, gm = left < kGroupTiles ? left : kGroupTiles;
+__device__ __forceinline__ Place place_of(const Product& P, const Experts& E, const Run& R, int t) {
+    // the last expert with base[x] <= t: 16 at a time, then one by one
+    const int lane = lane_id(), X = R.X;
+    int c = 0;
+    if (X > kWave) {
+        const int i = lane * 16;
+        c = (__popcll(ballot(i < X && E.base[i < X ? i : 0] <= t)) - 1) * 16;
+    }
+    const int i = c + lane;
+    const int x = c + __popcll(ballot((X <= kWave || lane < 16) && i < X && E.base[i < X ? i : 0] <= t)) - 1;
+    const int b0 = uniform(E.base[x]), all = uniform(E.base[x + 1]) - b0, in = t - b0;
     Place p;
     p.cnt = uniform(E.rows[x]);
-    // the expert's tiles share its rows evenly, in parts of 16
-    const int rows = ((p.cnt + mts - 1) / mts + 15) & ~15;
-    p.m0 = (g * kGroupTiles + r % gm) * rows;
-    p.n0 = r / gm * (GATED ? T::BN / 2 : T::BN);
+    int m = 0, n = in, rows = p.cnt;
+    if (all > R.ntn) {  // several row tiles
+        const int mts = all / R.ntn;
+        // row tiles in groups: within a group every row tile meets a weight tile before the next one
+        // comes, so that both stay in the XCD's cache while its CUs use them
+        const int g = mts > kGroupTiles ? in / (kGroupTiles * R.ntn) : 0, r = in - g * kGroupTiles * R.ntn;
+        const int left = mts - g * kGroupTiles, gm = left < kGroupTiles ? left : kGroupTiles;
+        n = r / gm;
+        m = g * kGroupTiles + r - n * gm;
+        rows = (p.cnt + mts - 1) / mts;
+    }
+    rows = (rows + 15) & ~15;  // the expert's tiles share its rows evenly, in parts of 16
+    p.m0 = m * rows;
+    p.n0 = n * (GATED ? T::BN / 2 : T::BN);
     p.end = p.m0 + rows < p.cnt ? p.m0 + rows : p.cnt;
-    const int d = P.rb + x / P.L;
-    p.e = (long)d * P.L + x % P.L;
+    const int d = P.rb + (P.rc > 1 ? x / P.L : 0);
+    p.e = (long)P.rb * P.L + x;
     p.row0 = (long)d * P.B + uniform(E.first[x]);
     return p;
 }
 
-__device__ __forceinline__ void load_lds16(const void* src, uint8_t* dst) {
+// Loads straight into LDS, 16 or 4 bytes a lane from `dst` on.  `dst` is an address that the compiler
+// cannot trace back to the ring (see lds_address): where it could, it made every LDS read wait for
+// all loads in flight.  The waits are wait_loads() and the barrier after it.
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
 }
-__device__ __forceinline__ void load_lds4(const void* src, uint8_t* dst) {
+__device__ __forceinline__ void load_lds4(const void* src, uint32_t dst) {
     __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 4, 0, 0);
+}
+__device__ __forceinline__ uint32_t lds_address(uint8_t* ring) {
+    uint32_t a = (uint32_t)(uintptr_t)(lds_void*)ring;
+    asm volatile("" : "+s"(a));
+    return a;
 }
 
 // A wave's loads of rows or of weights, stage after stage, tile after tile.  Lane l of a fill (8 rows of
@@ -170,102 +202,113 @@ __device__ __forceinline__ void load_lds4(const void* src, uint8_t* dst) {
 // of a 16-row part then spread over the LDS banks.  Rows past an expert's last repeat it; weight rows
 // past the last repeat it too.  For the gated product the weight rows of a tile alternate, 16 gate rows
 // and 16 up rows.
-template <bool FP8, bool GATED, class T>
+template <bool FP8, bool GATED, class T, bool ROWS>
 struct Loader {
-    const uint8_t *from, *ups;  // the tile's first row, or its first weight row and up row
-    uint32_t off[T::F];         // the lane's offset for each fill
-    const float* scale[2];      // the lane's scales (e4m3, waves that load rows)
-    int tile, k;                // next to load: stage k of a tile
+    static constexpr int kFills = ROWS ? T::FR : T::FW, kPer = (ROWS ? T::BM : T::BN) / 8;  // a wave's; a step's
+    const uint8_t* from;           // the tile's first row or weight row
+    long to_up;                    // gated: from a gate row to its up row
+    uint32_t off[kFills];          // the lane's offset for each fill
+    const float *rscale, *wscale;  // e4m3: of the tile's first row, of its expert's first weight block
+    int last;                      // the last row that may be read, from the first on
+    int block[2];                  // e4m3: the tile's weight blocks
+    int tile, k;                   // next to load: stage k of a tile
     int slot, group;
+    const uint8_t* src;            // of the stage being loaded
+    uint32_t to;
 
-    // Fill j of the wave's: fill i of the stage, its step and its first row.
-    __device__ __forceinline__ static int fill(int j, bool rows) { return (uniform(wave_id()) & 3) * (rows ? T::FR : T::FW) + j; }
+    // The first of the wave's fills of a stage; they are in a row.
+    __device__ __forceinline__ static int first() { return uniform(wave_id()) % (ROWS ? T::WR : T::WW) * kFills; }
 
-    __device__ __forceinline__ void aim(const Product& P, const Experts& E, int X, int ntn, bool rows) {
-        const Place p = place_of<T, GATED>(P, E, X, ntn, tile);
-        const int lane = lane_id();
+    __device__ __forceinline__ void begin(const Product& P, const Experts& E, const Run& R, int t) {
+        tile = t;
+        k = slot = group = 0;
+        aim(P, E, R);
+    }
+
+    __device__ __forceinline__ void aim(const Product& P, const Experts& E, const Run& R) {
+        const Place p = place_of<T, GATED>(P, E, R, tile);
         const int wrows = GATED ? 2 * P.C : P.C;
-        const int chunk = (lane & 7) ^ (lane >> 3), r8 = lane >> 3;
-        if (rows) {
-            from = ups = P.a + (p.row0 + p.m0) * P.KB;
-        } else {
-            from = P.w + (p.e * wrows + p.n0) * P.KB;
-            ups = from + (long)P.C * P.KB;
-        }
-        const int last = rows ? p.cnt - 1 - p.m0 : P.C - 1 - p.n0;
+        from = ROWS ? P.a + (p.row0 + p.m0) * P.KB : P.w + (p.e * wrows + p.n0) * P.KB;
+        to_up = (long)P.C * P.KB;
+        last = ROWS ? p.cnt - 1 - p.m0 : P.C - 1 - p.n0;
+        const int lane = lane_id(), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
-        for (int j = 0; j < T::F; ++j) {
-            const int i = fill(j, rows), per = (rows ? T::BM : T::BN) / 8;
-            const int kp = i / per, q = (i - kp * per) * 8;
-            const int r = (!rows && GATED ? (q >> 5) * 16 + (q & 15) : q) + r8;
-            off[j] = (uint32_t)(r < last ? r : last) * P.KB + kp * kStepBytes + chunk * 16;
+        for (int j = 0; j < kFills; ++j) {
+            const int i = first() + j, kp = T::KP == 1 ? 0 : i / kPer, q = (i - kp * kPer) * 8;
+            const int row = (GATED && !ROWS ? (q >> 5) * 16 + (q & 15) : q) + (lane >> 3);
+            off[j] = (uint32_t)(row < last ? row : last) * P.KB + kp * kStepBytes + chunk;
         }
-        if constexpr (FP8) {
-            if (rows) {
-                const int blocks = (wrows + 127) / 128;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int r = (uniform(wave_id()) + u * 4) * kWave + lane, j = r - T::BM;
-                    const int m = r < last ? r : last;
-                    int b = GATED ? (p.n0 + (j & 1) * P.C) / 128 : p.n0 / 128 + (j & 1);
-                    b = b < blocks ? b : blocks - 1;
-                    scale[u] = j < 0 || j > 1 ? P.as + (p.row0 + p.m0 + m) * P.KS : P.ws + (p.e * blocks + b) * P.KS;
-                }
-            }
+        if constexpr (FP8 && ROWS) {
+            const int blocks = (wrows + 127) / 128;
+            rscale = P.as + (p.row0 + p.m0) * P.KS;
+            wscale = P.ws + p.e * blocks * P.KS;
+            block[0] = p.n0 / 128;
+            block[1] = GATED ? (p.n0 + P.C) / 128 : p.n0 / 128 + 1;
+            block[1] = block[1] < blocks ? block[1] : blocks - 1;
         }
     }
 
-    // Loads the next stage into the ring and moves on.
-    __device__ __forceinline__ void load(const Product& P, const Experts& E, int X, int ntn, int tiles, int G, int stages,
-                                         uint8_t* ring, bool rows) {
-        const int lane = lane_id();
-        const int kb = k * T::KP * kStepBytes;
-        uint8_t* to = ring + (rows ? slot * T::kRowSlot : T::kWeightsAt + slot * T::kWeightSlot) + fill(0, rows) * 1024;
-        if constexpr (FP8) {
-            const int ks = k * T::KP;
-            if (rows && ks % 4 == 0) {
-                uint8_t* st = ring + T::kScalesAt + group * T::kScaleSlot;
+    // The next stage's scales, if it begins four steps.
+    __device__ __forceinline__ void load_scales(const Product& P, const Run& R) {
+        if constexpr (FP8 && ROWS) {
+            const int ks = k * T::KP, lane = lane_id();
+            if (ks % 4 != 0) return;
+            const uint32_t to = R.ring + T::kScalesAt + group * T::kScaleSlot;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int w = uniform(wave_id()) + u * 4;
-                    if (u * 4 >= T::kScaleLoads || w >= T::kScaleLoads) break;
-                    if (P.KS % 4 == 0) {  // 16-byte rows of scales
-                        load_lds16(scale[u] + ks, st + w * 1024);
-                    } else {
+            for (int u = 0; u < T::kScaleLoads; u += T::WR) {
+                const int w = uniform(wave_id()) + u;
+                if (w >= T::kScaleLoads) break;
+                // rows of the tile, then its weight blocks
+                const int r = w * kWave + lane, j = r - T::BM;
+                const float* of = j == 0   ? wscale + (long)block[0] * P.KS
+                                  : j == 1 ? wscale + (long)block[1] * P.KS
+                                           : rscale + (long)(r < last ? r : last) * P.KS;
+                if (P.KS % 4 == 0) {  // 16-byte rows of scales
+                    load_lds16(of + ks, to + w * 1024);
+                } else {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            load_lds4(scale[u] + (ks + q < P.KS ? ks + q : P.KS - 1), st + (q * T::kScaleLoads + w) * 256);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        load_lds4(of + (ks + q < P.KS ? ks + q : P.KS - 1), to + (q * T::kScaleLoads + w) * 256);
                 }
-                group = group == T::SR - 1 ? 0 : group + 1;
             }
+            group = group == T::kScaleSlots - 1 ? 0 : group + 1;
         }
-        const uint8_t *f = from + kb, *v = ups + kb;
-        const int mine = rows ? T::FR : T::FW, per = (rows ? T::BM : T::BN) / 8;
-        if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) {
+    }
+
+    // The wave's fills of the next stage: prepare() says whether they are to follow by load_fill(),
+    // one by one; at the end of a row it makes them itself, with zeros behind the end.
+    __device__ __forceinline__ bool prepare(const Product& P, const Run& R) {
+        const int kb = k * T::KP * kStepBytes;
+        src = from + kb;
+        to = R.ring + (ROWS ? slot * T::kRowSlot : T::kWeightsAt + slot * T::kWeightSlot) + first() * 1024;
+        if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) return true;
+        const int lane = lane_id(), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
-            for (int j = 0; j < T::F; ++j) {
-                const bool up = GATED && (fill(j, rows) % per) & 2;
-                if (T::FR == T::FW || j < mine) load_lds16((up ? v : f) + off[j], to + j * 1024);
-            }
-        } else {  // the last stage of a row: zeros from the row's end on
-            const int chunk = (lane & 7) ^ (lane >> 3);
-#pragma unroll
-            for (int j = 0; j < T::F; ++j) {
-                const int i = fill(j, rows);
-                const bool up = GATED && (i % per) & 2;
-                uint32_t o = off[j];
-                asm volatile("" : "+v"(o));  // keeps this path's addresses out of the other's registers
-                const bool in = kb + i / per * kStepBytes + chunk * 16 < P.KB;
-                if (T::FR == T::FW || j < mine) load_lds16(in ? (up ? v : f) + o : kZeros, to + j * 1024);
-            }
+        for (int j = 0; j < kFills; ++j) {
+            const bool in = kb + (first() + j) / kPer * kStepBytes + chunk < P.KB;
+            load_lds16(in ? src + up(j) + off[j] : kZeros, to + j * 1024);
         }
-        slot = slot == (rows ? T::SR : T::SW) - 1 ? 0 : slot + 1;
-        if (++k == stages) {
+        return false;
+    }
+    __device__ __forceinline__ long up(int j) const { return GATED && !ROWS && ((first() + j) % kPer & 2) ? to_up : 0; }
+    __device__ __forceinline__ void load_fill(int j) const { load_lds16(src + up(j) + off[j], to + j * 1024); }
+
+    __device__ __forceinline__ void advance(const Product& P, const Experts& E, const Run& R) {
+        slot = slot == (ROWS ? T::SR : T::SW) - 1 ? 0 : slot + 1;
+        if (++k == R.stages) {
             k = 0;
-            tile += G;
-            if (tile < tiles) aim(P, E, X, ntn, rows);
+            tile += R.G;
+            if (tile < R.tiles) aim(P, E, R);
         }
+    }
+
+    __device__ __forceinline__ void load(const Product& P, const Experts& E, const Run& R) {
+        load_scales(P, R);
+        if (prepare(P, R)) {
+#pragma unroll
+            for (int j = 0; j < kFills; ++j) load_fill(j);
+        }
+        advance(P, E, R);
     }
 };
 
@@ -368,6 +411,81 @@ __device__ __forceinline__ void write_tile(const Product& P, const Place& p, f32
     }
 }
 
+// What a wave of a tile reads of a stage, and its products.
+template <bool FP8, bool GATED, class T>
+struct Wave {
+    static constexpr int MT = T::MT, NT = T::NT;
+    f32x4 acc[NT][MT];
+    float sr[MT], sw[2];  // e4m3: scales of the wave's rows and weight blocks
+    i32x4 b[2][2];        // a part's rows and the next one's
+    int at_a, at_w, p0, p1;
+
+    __device__ __forceinline__ Wave() {
+        const int lane = lane_id(), wave = uniform(wave_id());
+        const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
+        const int r16 = lane & 15, g = lane >> 4;
+        // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
+        p0 = (g ^ (r16 & 7)) * 16;
+        p1 = p0 ^ 64;
+        at_a = (kp * T::BM + wm * 16 + r16) * kStepBytes;
+        at_w = T::kWeightsAt + (kp * T::BN + wn * NT * 16 + r16) * kStepBytes;
+        zero();
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void read_weights(const uint8_t* ring, int slot, int i, i32x4 (&w)[2]) const {
+        const uint8_t* t = ring + slot * T::kWeightSlot + at_w + i * 16 * kStepBytes;
+        w[0] = *(const i32x4*)(t + p0);
+        w[1] = *(const i32x4*)(t + p1);
+    }
+    __device__ __forceinline__ void read_rows(const uint8_t* ring, int slot, int j) {
+        const uint8_t* t = ring + slot * T::kRowSlot + at_a + j * T::WM * 16 * kStepBytes;
+        b[j & 1][0] = *(const i32x4*)(t + p0);
+        b[j & 1][1] = *(const i32x4*)(t + p1);
+    }
+    // The scales of stage k of a tile, in group `group` of the ring.
+    __device__ __forceinline__ void read_scales(const Product& P, const uint8_t* ring, int k, int group) {
+        const int lane = lane_id(), wave = uniform(wave_id());
+        const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
+        // 16 bytes a row, or the four steps apart
+        const bool by_row = P.KS % 4 == 0;
+        const int one = by_row ? 4 : 1;
+        const float* sc = (const float*)(ring + T::kScalesAt + group * T::kScaleSlot) +
+                          (k * T::KP + kp) % 4 * (by_row ? 1 : T::kScaleLoads * kWave);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sr[j] = sc[((j * T::WM + wm) * 16 + (lane & 15)) * one];
+        sw[0] = sc[(T::BM + (GATED ? 0 : wn * NT * 16 / 128)) * one];
+        sw[1] = GATED ? sc[(T::BM + 1) * one] : sw[0];
+    }
+    // Part j's products with the wave's weights.
+    __device__ __forceinline__ void multiply(const i32x4 (&w)[NT][2], int j) {
+        const i32x4 b0 = b[j & 1][0], b1 = b[j & 1][1];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if constexpr (FP8) {
+                const i32x8 A = __builtin_shufflevector(w[i][0], w[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+                const f32x4 q =
+                    __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+                const float s = sr[j] * sw[GATED ? (i & 1) : 0];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[i][j][u] = __builtin_fmaf(q[u], s, acc[i][j][u]);
+                // here, and not after all products: the partial sums would need registers of their own
+                asm volatile("" : "+v"(acc[i][j]));
+            } else {
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w[i][0]), __builtin_bit_cast(bf16x8, b0), acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w[i][1]), __builtin_bit_cast(bf16x8, b1), acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+};
+
 // The block's tiles, v, v + G, ..., as one run of stages: the loads run ahead of the products, across
 // the ends of tiles.
 template <bool FP8, bool GATED, class T>
@@ -375,39 +493,97 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
                                           int G) {
     static_assert(T::template bytes<FP8>() <= kRingBytes, "the ring");
     constexpr int MT = T::MT, NT = T::NT;
-    const int ntn = (P.C + (GATED ? T::BN / 2 : T::BN) - 1) / (GATED ? T::BN / 2 : T::BN);
-    const int tiles = E.base[X] * ntn;
-    if (v >= tiles) return;
-    const int stages = (P.KB + T::KP * kStepBytes - 1) / (T::KP * kStepBytes);
-    const long total = (long)((tiles - 1 - v) / G + 1) * stages;
-    const int lane = lane_id(), wave = uniform(wave_id());
+    Run R;
+    R.ring = lds_address(ring);
+    R.X = X;
+    R.G = G;
+    R.ntn = P.ntn[T::BN == 32 ? 0 : T::BN == 64 ? 1 : T::BN == 128 ? 2 : 3];
+    R.tiles = E.base[X];
+    if (v >= R.tiles) return;
+    R.stages = (P.KB + T::KP * kStepBytes - 1) / (T::KP * kStepBytes);
+    const int stages = R.stages;
+    const long total = (long)((R.tiles - 1 - v) / G + 1) * stages;
+    const int wave = uniform(wave_id());
     const bool rows = wave < T::WR, weights = wave >= kWaves - T::WW;
-    const int lead = rows ? T::kRowLead : T::kWeightLead;
-    Loader<FP8, GATED, T> L;
-    L.tile = v;
-    L.k = L.slot = L.group = 0;
-    if (rows || weights) {
-        L.aim(P, E, X, ntn, rows);
-        for (int n = 0; n < lead && n < total; ++n) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
+    Loader<FP8, GATED, T, true> LR;
+    Loader<FP8, GATED, T, false> LW;
+    if (weights) {
+        LW.begin(P, E, R, v);
+        for (int n = 0; n < T::kWeightLead && n < total; ++n) {
+            if (T::AHEAD && n == 1) {  // the order of the loop: weights, rows, weights
+                LR.begin(P, E, R, v);
+                LR.load(P, E, R);
+            }
+            LW.load(P, E, R);
+        }
     }
-    f32x4 acc[NT][MT];
-    auto zero = [&] {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    if (rows && !(T::AHEAD && total > 1)) {
+        LR.begin(P, E, R, v);
+        for (int n = 0; n < T::kRowLead && n < total; ++n) LR.load(P, E, R);
+    }
+    Wave<FP8, GATED, T> W;
+    i32x4 w[T::AHEAD ? 2 : 1][NT][2];
+    int rslot = 0, wslot = 0, group = -1, k = 0;
+    long n = 0;
+    auto scales = [&] {
+        if constexpr (FP8) {
+            if (k * T::KP % 4 == 0) group = group == T::kScaleSlots - 1 ? 0 : group + 1;
+            W.read_scales(P, ring, k, group);
+        }
     };
-    zero();
-    const int r16 = lane & 15, g = lane >> 4;
-    const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
-    // row r's chunk c lies at place c ^ (r % 8); a lane takes chunks g and g + 4 of its row
-    const int p0 = (g ^ (r16 & 7)) * 16, p1 = p0 ^ 64;
-    const int at_a = (kp * T::BM + wm * 16 + r16) * kStepBytes;
-    const int at_w = T::kWeightsAt + (kp * T::BN + wn * NT * 16 + r16) * kStepBytes;
-    constexpr int kNext = T::WM * 16 * kStepBytes;  // to the wave's next 16 rows
-    Place p = place_of<T, GATED>(P, E, X, ntn, v);
-    int ct = v, ck = 0, rslot = 0, wslot = 0, group = -1;
-    for (long n = 0; n < total; ++n) {
+    auto next = [&] {
+        rslot = rslot == T::SR - 1 ? 0 : rslot + 1;
+        ++n;
+        ++k;
+    };
+    // A stage: its weights are in w[now]; the next stage's come into w[1 - now] while the second half of
+    // the products runs.
+    auto stage_ahead = [&](auto now) {
+        constexpr int kNow = decltype(now)::value, kHalf = MT / 2, kRest = MT - MT / 2;
+        if (n + 1 < total) wait_loads<T::FW>();  // all but the next stage's weights
+        else wait_loads<0>();
+        lds_barrier();  // the stage's rows are there, the last stage's are done with
+        scales();
+        W.read_rows(ring, rslot, 0);
+        bool one_by_one = false;
+        if (n + 1 < total) {
+            LR.load_scales(P, R);
+            one_by_one = LR.prepare(P, R);
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            if (j == kHalf) {
+                if (n + 1 < total) {
+                    LR.advance(P, E, R);
+                    wait_loads<T::FR>();  // all but the next stage's rows
+                }
+                lds_barrier();  // the next stage's weights are there, this one's are in registers
+                wslot ^= 1;
+                one_by_one = n + 2 < total && LW.prepare(P, R);
+            }
+            if (j + 1 < MT) W.read_rows(ring, rslot, j + 1);
+            // the loads go out between the products, so that the waves do not queue for them
+            if (j < kHalf) {
+                if (one_by_one) {
+#pragma unroll
+                    for (int i = j * T::FR / kHalf; i < (j + 1) * T::FR / kHalf; ++i) LR.load_fill(i);
+                }
+            } else {
+#pragma unroll
+                for (int i = (j - kHalf) * NT / kRest; i < (j - kHalf + 1) * NT / kRest; ++i)
+                    W.read_weights(ring, wslot, i, w[1 - kNow][i]);
+                if (one_by_one) {
+#pragma unroll
+                    for (int i = (j - kHalf) * T::FW / kRest; i < (j - kHalf + 1) * T::FW / kRest; ++i) LW.load_fill(i);
+                }
+            }
+            W.multiply(w[kNow], j);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (n + 2 < total) LW.advance(P, E, R);
+        next();
+    };
+    auto stage = [&] {
         if (rows) {
             if (n + T::kRowLead <= total) wait_loads<(T::kRowLead - 1) * T::FR>();
             else wait_loads<0>();
@@ -416,76 +592,62 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
             else wait_loads<0>();
         }
         lds_barrier();
-        const bool more = n + lead < total;
-        if (more && (rows || (weights && !T::EARLY))) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
-        const uint8_t* ta = ring + rslot * T::kRowSlot + at_a;
-        const uint8_t* tw = ring + wslot * T::kWeightSlot + at_w;
-        float sr[MT], sw[2];
-        if constexpr (FP8) {
-            const int ks = ck * T::KP;
-            if (ks % 4 == 0) group = group == T::SR - 1 ? 0 : group + 1;
-            // 16 bytes a row, or the four steps apart
-            const bool by_row = P.KS % 4 == 0;
-            const int one = by_row ? 4 : 1;
-            const float* sc = (const float*)(ring + T::kScalesAt + group * T::kScaleSlot) +
-                              (ks + kp) % 4 * (by_row ? 1 : T::kScaleLoads * kWave);
+        auto load = [&] {
+            if (rows && n + T::kRowLead < total) LR.load(P, E, R);
+            asm volatile("");  // the two are not to be merged into one that takes its loader by address
+            if (weights && n + T::kWeightLead < total) LW.load(P, E, R);
+        };
+        if constexpr (!T::EARLY) load();
+        scales();
 #pragma unroll
-            for (int j = 0; j < MT; ++j) sr[j] = sc[((j * T::WM + wm) * 16 + r16) * one];
-            sw[0] = sc[(T::BM + (GATED ? 0 : wn * NT * 16 / 128)) * one];
-            sw[1] = GATED ? sc[(T::BM + 1) * one] : sw[0];
-        }
-        i32x4 w[NT][2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            w[i][0] = *(const i32x4*)(tw + i * 16 * kStepBytes + p0);
-            w[i][1] = *(const i32x4*)(tw + i * 16 * kStepBytes + p1);
-        }
-        i32x4 b[2][2];
-        b[0][0] = *(const i32x4*)(ta + p0);
-        b[0][1] = *(const i32x4*)(ta + p1);
+        for (int i = 0; i < NT; ++i) W.read_weights(ring, wslot, i, w[0][i]);
         if constexpr (T::EARLY) {
-            lds_barrier();  // every wave has its weights
-            if (more && weights) L.load(P, E, X, ntn, tiles, G, stages, ring, rows);
+            static_assert(MT <= 2, "a stage's rows in registers");
+#pragma unroll
+            for (int j = 0; j < MT; ++j) W.read_rows(ring, rslot, j);
+            lds_barrier();  // the stage is in registers
+            load();
+        } else {
+            W.read_rows(ring, rslot, 0);
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             // the next part's rows are read while this one's products run; no further ahead, for the
             // registers' sake
-            if (j + 1 < MT) {
-                b[(j + 1) & 1][0] = *(const i32x4*)(ta + (j + 1) * kNext + p0);
-                b[(j + 1) & 1][1] = *(const i32x4*)(ta + (j + 1) * kNext + p1);
-            }
-            const i32x4 b0 = b[j & 1][0], b1 = b[j & 1][1];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if constexpr (FP8) {
-                    const i32x8 A = __builtin_shufflevector(w[i][0], w[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-                    const f32x4 q =
-                        __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-                    const float s = sr[j] * sw[GATED ? (i & 1) : 0];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[i][j][u] = __builtin_fmaf(q[u], s, acc[i][j][u]);
-                    // here, and not after all products: the partial sums would need registers of their own
-                    asm volatile("" : "+v"(acc[i][j]));
-                } else {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, w[i][0]), __builtin_bit_cast(bf16x8, b0), acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, w[i][1]), __builtin_bit_cast(bf16x8, b1), acc[i][j], 0, 0, 0);
-                }
-            }
+            if (!T::EARLY && j + 1 < MT) W.read_rows(ring, rslot, j + 1);
+            W.multiply(w[0], j);
             __builtin_amdgcn_sched_barrier(0);
         }
-        rslot = rslot == T::SR - 1 ? 0 : rslot + 1;
         wslot = wslot == T::SW - 1 ? 0 : wslot + 1;
-        if (++ck == stages) {
-            write_tile<FP8, GATED, T>(P, p, acc, epi);
-            zero();
-            ck = 0;
-            ct += G;
-            if (ct < tiles) p = place_of<T, GATED>(P, E, X, ntn, ct);
+        next();
+    };
+    if constexpr (T::AHEAD) {
+        if (total > 1) wait_loads<T::FW + T::FR>();  // the first weights; the scales among the rest are few
+        else wait_loads<0>();
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < NT; ++i) W.read_weights(ring, 0, i, w[0][i]);
+    }
+    for (int t = v; t < R.tiles; t += G) {
+        if constexpr (T::AHEAD) {
+            for (k = 0; k + 1 < stages;) {
+                stage_ahead(std::integral_constant<int, 0>());
+                stage_ahead(std::integral_constant<int, 1>());
+            }
+            if (k < stages) {
+                stage_ahead(std::integral_constant<int, 0>());
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) w[0][i][u] = w[1][i][u];
+            }
+            write_tile<FP8, GATED, T>(P, place_of<T, GATED>(P, E, R, t), W.acc, epi);
+        } else {
+            const Place p = place_of<T, GATED>(P, E, R, t);
+            for (k = 0; k < stages;) stage();
+            write_tile<FP8, GATED, T>(P, p, W.acc, epi);
         }
+        W.zero();
     }
     lds_barrier();
 }
@@ -493,7 +655,7 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
 // The tiles, from few rows and columns to many.  The gated product needs two 16-row parts of a tile's
 // weight rows in each wave (gate and up), and with e4m3 operands 256 of them in a tile: it quantises
 // blocks of 128 output columns.
-constexpr int kLevels = 4;
+constexpr int kLevels = 5;
 enum { kPlain, kGated, kWide };
 template <int KIND, int I> struct TileOf;
 template <> struct TileOf<kPlain, 0> { typedef Tile<16, 32, 1, 2, 4, 3, 7> type; };
@@ -507,58 +669,44 @@ template <> struct TileOf<kGated, 3> { typedef Tile<32, 64, 2, 2, 2, 3, 7> type;
 template <int KIND> struct TileOf<KIND, 4> { typedef Tile<64, 64, 2, 2, 2, 3, 5> type; };
 template <int KIND> struct TileOf<KIND, 5> { typedef Tile<64, 128, 2, 4, 1, 3, 7> type; };
 template <int KIND> struct TileOf<KIND, 6> { typedef Tile<128, 128, 2, 4, 1, 3, 5> type; };
-template <> struct TileOf<kWide, 3> { typedef Tile<16, 256, 1, 8, 1, 4, 4> type; };
-template <> struct TileOf<kWide, 4> { typedef Tile<32, 256, 1, 8, 1, 3, 4> type; };
-template <> struct TileOf<kWide, 5> { typedef Tile<64, 256, 1, 8, 1, 3, 3> type; };
-template <int KIND> struct TileOf<KIND, 7> { typedef Tile<128, 256, 2, 4, 1, 2, 3> type; };
-template <int KIND> struct TileOf<KIND, 8> { typedef Tile<160, 256, 2, 4, 1, 2, 2, true> type; };
-template <int KIND> struct TileOf<KIND, 9> { typedef Tile<192, 256, 2, 4, 1, 2, 2, true> type; };
-template <int KIND> struct TileOf<KIND, 10> { typedef Tile<256, 256, 2, 4, 1, 2, 2, true> type; };
+template <int KIND> struct TileOf<KIND, 7> { typedef Tile<192, 128, 2, 4, 1, 2, 5> type; };
+template <> struct TileOf<kWide, 4> { typedef Tile<16, 256, 1, 8, 1, 3, 4, kEarly> type; };
+template <> struct TileOf<kWide, 5> { typedef Tile<32, 256, 1, 8, 1, 2, 4, kEarly> type; };
+template <> struct TileOf<kWide, 6> { typedef Tile<64, 256, 1, 8, 1, 3, 3> type; };
+template <int KIND> struct TileOf<KIND, 8> { typedef Tile<128, 256, 2, 4, 1, 2, 3> type; };
+template <int KIND> struct TileOf<KIND, 9> { typedef Tile<192, 256, 2, 4, 1, 2, 2, kAhead> type; };
+template <int KIND> struct TileOf<KIND, 10> { typedef Tile<256, 256, 2, 4, 1, 2, 2, kAhead> type; };
 
-// At each level an expert's rows make as few row tiles as fit `most` rows each (0: the largest tile;
-// further levels smaller ones, for products that would leave CUs without a tile), and the tiles take
-// the least height that holds their even share.
+// A product takes the first level whose tiles are enough for most CUs: level 0 has the largest tiles,
+// further levels smaller ones.  At a level an expert's rows make as few row tiles as fit its most rows
+// each, and the tiles take the least height that holds their even share.
+constexpr int kEnoughTiles = 192;
+struct Choice {
+    int mts, tile, width;  // row tiles, their kind (-1: no rows), and log2(weight rows) - 5
+};
 template <bool WIDE>
-__device__ __forceinline__ int level_rows(int level) {
-    return level == 0 ? 256 : level == 1 ? 128 : WIDE || level == 2 ? 64 : 32;
-}
-template <bool WIDE>
-__device__ __forceinline__ int row_tiles(int rows, int level) {
-    return (rows + level_rows<WIDE>(level) - 1) / level_rows<WIDE>(level);
-}
-template <bool WIDE>
-__device__ __forceinline__ int tile_of(int rows, int level) {
-    const int mts = row_tiles<WIDE>(rows, level), n = (rows + mts - 1) / (mts > 0 ? mts : 1);
-    if (WIDE) return n > 192 ? 10 : n > 160 ? 9 : n > 128 ? 8 : n > 64 ? 7 : n > 32 ? 5 : n > 16 ? 4 : 3;
-    if (level == 3) return n > 16 ? 1 : 0;
-    if (n <= 32) return n > 16 ? 3 : 2;
-    if (level == 2) return 4;
-    if (n <= 64) return 5;
-    return level == 1 ? 6 : n > 192 ? 10 : n > 160 ? 9 : n > 128 ? 8 : 7;
-}
-
-// Columns of weight rows of a tile, and the time of a step over K, in cycles.
-template <bool WIDE>
-__device__ __forceinline__ int tile_width(int i) {
-    return WIDE || i >= 7 ? 256 : i >= 5 ? 128 : i >= 2 ? 64 : 32;
-}
-template <bool WIDE>
-__device__ __forceinline__ int tile_time(int i, int rows) {
-    return tile_width<WIDE>(i) * 4 + rows * tile_width<WIDE>(i) / 32 + 150;
-}
-
-// base[x] = row tiles of tile i of the experts before x.
-template <bool WIDE>
-__device__ __forceinline__ void scan_tiles(const int* rows, int level, int tile, int X, int* base, int* part) {
-    lds_barrier();  // the last tile's run is done with base
-    int n[2], v = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int x = 2 * threadIdx.x + i;
-        n[i] = rows[i] > 0 && tile_of<WIDE>(rows[i], level) == tile ? row_tiles<WIDE>(rows[i], level) : 0;
-        v += n[i];
+__device__ __forceinline__ Choice choose(int rows, int level) {
+    Choice c;
+    if (WIDE) c.mts = level == 0 ? (rows + 255) >> 8 : level == 1 ? (rows + 127) >> 7 : (rows + 63) >> 6;
+    else c.mts = level == 0 ? (rows + 255) >> 8 : level == 1 ? (rows + 191) / 192 : level <= 3 ? (rows + 63) >> 6 : (rows + 31) >> 5;
+    const int m = c.mts;
+    const bool few = rows <= 16 * m, some = rows <= 32 * m, half = rows <= 64 * m, more = rows <= 128 * m;
+    if (WIDE) {
+        c.tile = few ? 4 : some ? 5 : half ? 6 : 8;
+        c.width = 3;
+    } else {
+        c.tile = level == 4 ? (few ? 0 : 1) : few ? 2 : some ? 3 : half ? (level == 3 ? 4 : 5) : level == 1 ? 6 : 8;
+        c.width = c.tile < 2 ? 0 : c.tile < 5 ? 1 : c.tile < 8 ? 2 : 3;
     }
-    const int inc = wave_incl_scan(v);
+    if (!more) c.tile = c.tile == 6 ? 7 : rows <= 192 * m ? 9 : 10;
+    if (rows == 0) c.tile = -1;
+    return c;
+}
+
+// base[x] = tiles of the experts before x, of which this thread's two have n[0] and n[1].
+__device__ __forceinline__ void scan_tiles(const int (&n)[2], int X, int* base, int* part) {
+    lds_barrier();  // the last kind's run is done with base
+    const int v = n[0] + n[1], inc = wave_incl_scan(v);
     if (lane_id() == kWave - 1) part[wave_id()] = inc;
     lds_barrier();
     int before = inc - v;
@@ -581,18 +729,14 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
     __shared__ __attribute__((aligned(16))) float epi[kEpiBytes / 4];
     __shared__ Experts E;
     __shared__ int part[kWaves];
-    __shared__ unsigned long long sum[kLevels];
-    __shared__ int most[kLevels];
+    __shared__ int sum[kLevels];
     __shared__ int present;
     const int X = P.rc * P.L, G = gridDim.x;
     // blocks of one XCD (the hardware deals blocks to the eight in turn) take neighbouring tiles
     const int per = G / 8, b = blockIdx.x;
     const int v = b < per * 8 ? b % 8 * per + b / 8 : b;
-    if (threadIdx.x < kLevels) {
-        sum[threadIdx.x] = 0;
-        most[threadIdx.x] = 0;
-    }
-    if (threadIdx.x == 0) present = 0;
+    if (threadIdx.x < kLevels) sum[threadIdx.x] = 0;
+    if (threadIdx.x == kLevels) present = 0;
     lds_barrier();
     int rows[2] = {0, 0};
 #pragma unroll
@@ -603,66 +747,46 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
             E.rows[x] = rows[i];
         }
     }
-    // the level whose tiles end first: their times over all blocks, or the longest of them
+    // (this part runs once: loops kept rolled, so that little code has to be fetched for it)
     constexpr int levels = WIDE ? 3 : kLevels;
-    for (int l = 0; l < levels; ++l) {
-        long t = 0;
-        int longest = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (rows[i] == 0) continue;
-            const int tile = tile_of<WIDE>(rows[i], l), mts = row_tiles<WIDE>(rows[i], l);
-            const int cols = GATED ? tile_width<WIDE>(tile) / 2 : tile_width<WIDE>(tile);
-            const int one = tile_time<WIDE>(tile, (rows[i] + mts - 1) / mts);
-            t += (long)mts * ((P.C + cols - 1) / cols) * one;
-            longest = one > longest ? one : longest;
-        }
-        if (longest) {
-            atomicAdd(&sum[l], (unsigned long long)t);
-            atomicMax(&most[l], longest);
-        }
+    auto tiles_of = [&](const Choice& c) {
+        const int w = c.width;
+        return c.mts * (w == 0 ? P.ntn[0] : w == 1 ? P.ntn[1] : w == 2 ? P.ntn[2] : P.ntn[3]);
+    };
+    if (rows[0] + rows[1]) {
+#pragma unroll 1
+        for (int l = 0; l < levels - 1; ++l) atomicAdd(&sum[l], tiles_of(choose<WIDE>(rows[0], l)) + tiles_of(choose<WIDE>(rows[1], l)));
     }
     lds_barrier();
     int level = 0;
-    long least = 0;
-    for (int l = 0; l < levels; ++l) {
-        const long all = (long)sum[l] / G, t = all > most[l] ? all : most[l];
-        if (l == 0 || t < least) {
-            level = l;
-            least = t;
-        }
-    }
-    level = uniform(level);
-#ifdef MOE_EXPERT_LEVEL
-    level = MOE_EXPERT_LEVEL;
-#endif
-    int bits = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (rows[i] > 0) bits |= 1 << tile_of<WIDE>(rows[i], level);
+#pragma unroll 1
+    while (level < levels - 1 && sum[level] < kEnoughTiles) ++level;
+    const Choice mine[2] = {choose<WIDE>(rows[0], level), choose<WIDE>(rows[1], level)};
+    const int count[2] = {tiles_of(mine[0]), tiles_of(mine[1])};
+    const int bits = (rows[0] ? 1 << mine[0].tile : 0) | (rows[1] ? 1 << mine[1].tile : 0);
     if (bits) atomicOr(&present, bits);
     lds_barrier();
     const int all = uniform(present);
-    int done = 0;  // tiles so far: the next kind of tile begins at the block after them
+    int done = 0;  // the block after the last tile's: the next kind of tile begins there
     auto run = [&](auto tile, int i) {
         typedef decltype(tile) T;
         if (!(all >> i & 1)) return;
-        scan_tiles<WIDE>(rows, level, i, X, E.base, part);
-        int w = v - done % G;
+        const int n[2] = {mine[0].tile == i ? count[0] : 0, mine[1].tile == i ? count[1] : 0};
+        scan_tiles(n, X, E.base, part);
+        int w = v - done;
         w = w < 0 ? w + G : w;
         run_tiles<FP8, GATED, T>(P, ring, E, epi, X, w, G);
-        const int cols = GATED ? T::BN / 2 : T::BN;
-        done += uniform(E.base[X]) * ((P.C + cols - 1) / cols);
+        done = (done + uniform(E.base[X])) % G;
     };
     run(typename TileOf<KIND, 10>::type(), 10);
     run(typename TileOf<KIND, 9>::type(), 9);
     run(typename TileOf<KIND, 8>::type(), 8);
-    run(typename TileOf<KIND, 7>::type(), 7);
-    if constexpr (!WIDE) run(typename TileOf<KIND, 6>::type(), 6);
+    if constexpr (!WIDE) run(typename TileOf<KIND, 7>::type(), 7);
+    run(typename TileOf<KIND, 6>::type(), 6);
     run(typename TileOf<KIND, 5>::type(), 5);
     run(typename TileOf<KIND, 4>::type(), 4);
-    run(typename TileOf<KIND, 3>::type(), 3);
     if constexpr (!WIDE) {
+        run(typename TileOf<KIND, 3>::type(), 3);
         run(typename TileOf<KIND, 2>::type(), 2);
         run(typename TileOf<KIND, 1>::type(), 1);
         run(typename TileOf<KIND, 0>::type(), 0);
@@ -691,6 +815,10 @@ hipError_t launch_experts(const Dims& D, bool gated, int K, int C, const void* a
     P.L = D.L;
     P.rb = D.rb;
     P.rc = D.rc;
+    for (int i = 0; i < 4; ++i) {
+        const int cols = (gated ? 16 : 32) << i;
+        P.ntn[i] = (C + cols - 1) / cols;
+    }
     // one block a CU (each takes nearly all of its LDS); fewer if there cannot be as many tiles
     const long mts = (recv_rows_bound(D) + 15) / 16 + (long)D.rc * D.L;
     const int cols = D.fp8 && gated ? 128 : gated ? 16 : 32;
