@@ -5,8 +5,6 @@
 //             v[q][c] = sum_b as[q][b] ws[e][c/128][b] p_b[q][c]       e4m3: p_b the fp32 sum over the
 //                                                                      128 values k of block b
 //   gated     h = g / (1 + exp(-g)) * u,  g = v[q][c], u = v[q][I + c]
-#include <type_traits>
-
 #include "common.hpp"
 
 namespace moe {
@@ -48,28 +46,24 @@ __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
 
 // The shape of a tile: BM rows x BN weight rows by WM x WN x KP waves (KP: waves that share a
 // tile's part and take every KP-th step).  A stage is KP steps.  The rows go through a ring of SR
-// stages, the weights through one of SW.  Small tiles: the first waves load the rows and the last four
-// the weights; a wave waits for its loads in their order, so rows (short way, from the cache) and
-// weights (long way, from memory) wait apart.  EARLY: a stage is read into registers whole and its
-// place refilled before its products, which leaves one stage more in flight.  AHEAD (tiles bound by
-// arithmetic): every wave loads its share of both between its products; a stage's weights are read
-// into registers during the stage before, and their place in the ring is refilled from the middle of
-// the stage on.
-enum { kRing, kEarly, kAhead };
+// stages, loaded by the first waves, the weights through one of SW, loaded by the last four: a wave
+// waits for its loads in their order, so rows (short way, from the cache) and weights (long way, from
+// memory) wait apart.  kEarly: a stage is read into registers whole and its place refilled before its
+// products, which leaves one stage more in flight; kEarlyWeights: the same for the weights alone.
+enum { kRing, kEarly, kEarlyWeights };
 template <int BM_, int BN_, int WM_, int WN_, int KP_, int SR_, int SW_, int MODE = kRing>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KP = KP_, SR = SR_, SW = SW_;
-    static constexpr bool AHEAD = MODE == kAhead, EARLY = MODE == kEarly;
-    static_assert(!AHEAD || (SR == 2 && SW == 2 && KP == 1), "two stages");
+    static constexpr bool EARLY = MODE == kEarly, EARLYW = MODE == kEarlyWeights;
     static_assert(WM * WN * KP == kWaves, "eight waves");
     static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 parts of a wave
     // waves that load rows and weights, and the loads of 8 rows that each makes, a stage
     static constexpr int kRowFills = KP * BM / 8, kWeightFills = KP * BN / 8;
-    static constexpr int WR = AHEAD ? kWaves : kRowFills < 4 ? kRowFills : 4, WW = AHEAD ? kWaves : 4;
+    static constexpr int WR = kRowFills < 4 ? kRowFills : 4, WW = 4;
     static constexpr int FR = kRowFills / WR, FW = kWeightFills / WW;
     static_assert(FR * WR == kRowFills && FW * WW == kWeightFills, "whole fills");
     // stages that the loads run ahead
-    static constexpr int kRowLead = EARLY ? SR : SR - 1, kWeightLead = AHEAD || EARLY ? SW : SW - 1;
+    static constexpr int kRowLead = EARLY ? SR : SR - 1, kWeightLead = MODE == kRing ? SW - 1 : SW;
     static constexpr int kRowSlot = KP * BM * kStepBytes, kWeightSlot = KP * BN * kStepBytes;
     // e4m3: the scales of four steps, 16 bytes for each row and for the tile's two weight blocks
     static constexpr int kScaleLoads = (BM + 2 + kWave - 1) / kWave, kScaleSlot = kScaleLoads * kWave * 16;
@@ -213,8 +207,6 @@ struct Loader {
     int block[2];                  // e4m3: the tile's weight blocks
     int tile, k;                   // next to load: stage k of a tile
     int slot, group;
-    const uint8_t* src;            // of the stage being loaded
-    uint32_t to;
 
     // The first of the wave's fills of a stage; they are in a row.
     __device__ __forceinline__ static int first() { return uniform(wave_id()) % (ROWS ? T::WR : T::WW) * kFills; }
@@ -275,23 +267,25 @@ struct Loader {
         }
     }
 
-    // The wave's fills of the next stage: prepare() says whether they are to follow by load_fill(),
-    // one by one; at the end of a row it makes them itself, with zeros behind the end.
-    __device__ __forceinline__ bool prepare(const Product& P, const Run& R) {
-        const int kb = k * T::KP * kStepBytes;
-        src = from + kb;
-        to = R.ring + (ROWS ? slot * T::kRowSlot : T::kWeightsAt + slot * T::kWeightSlot) + first() * 1024;
-        if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) return true;
-        const int lane = lane_id(), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-#pragma unroll
-        for (int j = 0; j < kFills; ++j) {
-            const bool in = kb + (first() + j) / kPer * kStepBytes + chunk < P.KB;
-            load_lds16(in ? src + up(j) + off[j] : kZeros, to + j * 1024);
-        }
-        return false;
-    }
     __device__ __forceinline__ long up(int j) const { return GATED && !ROWS && ((first() + j) % kPer & 2) ? to_up : 0; }
-    __device__ __forceinline__ void load_fill(int j) const { load_lds16(src + up(j) + off[j], to + j * 1024); }
+
+    // The wave's fills of the next stage.
+    __device__ __forceinline__ void load_fills(const Product& P, const Run& R) const {
+        const int kb = k * T::KP * kStepBytes;
+        const uint8_t* src = from + kb;
+        const uint32_t to = R.ring + (ROWS ? slot * T::kRowSlot : T::kWeightsAt + slot * T::kWeightSlot) + first() * 1024;
+        if ((FP8 && T::KP == 1) || kb + T::KP * kStepBytes <= P.KB) {
+#pragma unroll
+            for (int j = 0; j < kFills; ++j) load_lds16(src + up(j) + off[j], to + j * 1024);
+        } else {  // the last stage of a row: zeros from the row's end on
+            const int lane = lane_id(), chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+            for (int j = 0; j < kFills; ++j) {
+                const bool in = kb + (first() + j) / kPer * kStepBytes + chunk < P.KB;
+                load_lds16(in ? src + up(j) + off[j] : kZeros, to + j * 1024);
+            }
+        }
+    }
 
     __device__ __forceinline__ void advance(const Product& P, const Experts& E, const Run& R) {
         slot = slot == (ROWS ? T::SR : T::SW) - 1 ? 0 : slot + 1;
@@ -304,10 +298,7 @@ struct Loader {
 
     __device__ __forceinline__ void load(const Product& P, const Experts& E, const Run& R) {
         load_scales(P, R);
-        if (prepare(P, R)) {
-#pragma unroll
-            for (int j = 0; j < kFills; ++j) load_fill(j);
-        }
+        load_fills(P, R);
         advance(P, E, R);
     }
 };
@@ -509,20 +500,14 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
     Loader<FP8, GATED, T, false> LW;
     if (weights) {
         LW.begin(P, E, R, v);
-        for (int n = 0; n < T::kWeightLead && n < total; ++n) {
-            if (T::AHEAD && n == 1) {  // the order of the loop: weights, rows, weights
-                LR.begin(P, E, R, v);
-                LR.load(P, E, R);
-            }
-            LW.load(P, E, R);
-        }
+        for (int n = 0; n < T::kWeightLead && n < total; ++n) LW.load(P, E, R);
     }
-    if (rows && !(T::AHEAD && total > 1)) {
+    if (rows) {
         LR.begin(P, E, R, v);
         for (int n = 0; n < T::kRowLead && n < total; ++n) LR.load(P, E, R);
     }
     Wave<FP8, GATED, T> W;
-    i32x4 w[T::AHEAD ? 2 : 1][NT][2];
+    i32x4 w[NT][2];
     int rslot = 0, wslot = 0, group = -1, k = 0;
     long n = 0;
     auto scales = [&] {
@@ -536,53 +521,6 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
         ++n;
         ++k;
     };
-    // A stage: its weights are in w[now]; the next stage's come into w[1 - now] while the second half of
-    // the products runs.
-    auto stage_ahead = [&](auto now) {
-        constexpr int kNow = decltype(now)::value, kHalf = MT / 2, kRest = MT - MT / 2;
-        if (n + 1 < total) wait_loads<T::FW>();  // all but the next stage's weights
-        else wait_loads<0>();
-        lds_barrier();  // the stage's rows are there, the last stage's are done with
-        scales();
-        W.read_rows(ring, rslot, 0);
-        bool one_by_one = false;
-        if (n + 1 < total) {
-            LR.load_scales(P, R);
-            one_by_one = LR.prepare(P, R);
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            if (j == kHalf) {
-                if (n + 1 < total) {
-                    LR.advance(P, E, R);
-                    wait_loads<T::FR>();  // all but the next stage's rows
-                }
-                lds_barrier();  // the next stage's weights are there, this one's are in registers
-                wslot ^= 1;
-                one_by_one = n + 2 < total && LW.prepare(P, R);
-            }
-            if (j + 1 < MT) W.read_rows(ring, rslot, j + 1);
-            // the loads go out between the products, so that the waves do not queue for them
-            if (j < kHalf) {
-                if (one_by_one) {
-#pragma unroll
-                    for (int i = j * T::FR / kHalf; i < (j + 1) * T::FR / kHalf; ++i) LR.load_fill(i);
-                }
-            } else {
-#pragma unroll
-                for (int i = (j - kHalf) * NT / kRest; i < (j - kHalf + 1) * NT / kRest; ++i)
-                    W.read_weights(ring, wslot, i, w[1 - kNow][i]);
-                if (one_by_one) {
-#pragma unroll
-                    for (int i = (j - kHalf) * T::FW / kRest; i < (j - kHalf + 1) * T::FW / kRest; ++i) LW.load_fill(i);
-                }
-            }
-            W.multiply(w[kNow], j);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (n + 2 < total) LW.advance(P, E, R);
-        next();
-    };
     auto stage = [&] {
         if (rows) {
             if (n + T::kRowLead <= total) wait_loads<(T::kRowLead - 1) * T::FR>();
@@ -595,12 +533,12 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
         auto load = [&] {
             if (rows && n + T::kRowLead < total) LR.load(P, E, R);
             asm volatile("");  // the two are not to be merged into one that takes its loader by address
-            if (weights && n + T::kWeightLead < total) LW.load(P, E, R);
+            if (!T::EARLYW && weights && n + T::kWeightLead < total) LW.load(P, E, R);
         };
         if constexpr (!T::EARLY) load();
         scales();
 #pragma unroll
-        for (int i = 0; i < NT; ++i) W.read_weights(ring, wslot, i, w[0][i]);
+        for (int i = 0; i < NT; ++i) W.read_weights(ring, wslot, i, w[i]);
         if constexpr (T::EARLY) {
             static_assert(MT <= 2, "a stage's rows in registers");
 #pragma unroll
@@ -609,44 +547,26 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
             load();
         } else {
             W.read_rows(ring, rslot, 0);
+            if constexpr (T::EARLYW) {
+                lds_barrier();  // the stage's weights are in registers
+                if (weights && n + T::kWeightLead < total) LW.load(P, E, R);
+            }
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             // the next part's rows are read while this one's products run; no further ahead, for the
             // registers' sake
             if (!T::EARLY && j + 1 < MT) W.read_rows(ring, rslot, j + 1);
-            W.multiply(w[0], j);
+            W.multiply(w, j);
             __builtin_amdgcn_sched_barrier(0);
         }
         wslot = wslot == T::SW - 1 ? 0 : wslot + 1;
         next();
     };
-    if constexpr (T::AHEAD) {
-        if (total > 1) wait_loads<T::FW + T::FR>();  // the first weights; the scales among the rest are few
-        else wait_loads<0>();
-        lds_barrier();
-#pragma unroll
-        for (int i = 0; i < NT; ++i) W.read_weights(ring, 0, i, w[0][i]);
-    }
     for (int t = v; t < R.tiles; t += G) {
-        if constexpr (T::AHEAD) {
-            for (k = 0; k + 1 < stages;) {
-                stage_ahead(std::integral_constant<int, 0>());
-                stage_ahead(std::integral_constant<int, 1>());
-            }
-            if (k < stages) {
-                stage_ahead(std::integral_constant<int, 0>());
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) w[0][i][u] = w[1][i][u];
-            }
-            write_tile<FP8, GATED, T>(P, place_of<T, GATED>(P, E, R, t), W.acc, epi);
-        } else {
-            const Place p = place_of<T, GATED>(P, E, R, t);
-            for (k = 0; k < stages;) stage();
-            write_tile<FP8, GATED, T>(P, p, W.acc, epi);
-        }
+        const Place p = place_of<T, GATED>(P, E, R, t);
+        for (k = 0; k < stages;) stage();
+        write_tile<FP8, GATED, T>(P, p, W.acc, epi);
         W.zero();
     }
     lds_barrier();
@@ -674,15 +594,19 @@ template <> struct TileOf<kWide, 4> { typedef Tile<16, 256, 1, 8, 1, 3, 4, kEarl
 template <> struct TileOf<kWide, 5> { typedef Tile<32, 256, 1, 8, 1, 2, 4, kEarly> type; };
 template <> struct TileOf<kWide, 6> { typedef Tile<64, 256, 1, 8, 1, 3, 3> type; };
 template <int KIND> struct TileOf<KIND, 8> { typedef Tile<128, 256, 2, 4, 1, 2, 3> type; };
-template <int KIND> struct TileOf<KIND, 9> { typedef Tile<192, 256, 2, 4, 1, 2, 2, kAhead> type; };
-template <int KIND> struct TileOf<KIND, 10> { typedef Tile<256, 256, 2, 4, 1, 2, 2, kAhead> type; };
+template <int KIND> struct TileOf<KIND, 9> { typedef Tile<160, 256, 2, 4, 1, 2, 2, kEarlyWeights> type; };
+template <int KIND> struct TileOf<KIND, 10> { typedef Tile<192, 256, 2, 4, 1, 2, 2, kEarlyWeights> type; };
+template <int KIND> struct TileOf<KIND, 11> { typedef Tile<256, 256, 2, 4, 1, 2, 2, kEarlyWeights> type; };
 
-// A product takes the first level whose tiles are enough for most CUs: level 0 has the largest tiles,
+// A product takes the first level that has work for most CUs: its tiles together cost kEnough times
+// the dearest of them (the last but one level: kEnoughSmall times).  Level 0 has the largest tiles,
 // further levels smaller ones.  At a level an expert's rows make as few row tiles as fit its most rows
 // each, and the tiles take the least height that holds their even share.
-constexpr int kEnoughTiles = 192;
+constexpr int kEnough = 192, kEnoughSmall = 64;
 struct Choice {
-    int mts, tile, width;  // row tiles, their kind (-1: no rows), and log2(weight rows) - 5
+    int mts, tile;  // row tiles, and their kind (-1: no rows)
+    int width;      // log2(weight rows) - 5
+    int cost;       // of a tile, a step: its weights and its products
 };
 template <bool WIDE>
 __device__ __forceinline__ Choice choose(int rows, int level) {
@@ -690,34 +614,41 @@ __device__ __forceinline__ Choice choose(int rows, int level) {
     if (WIDE) c.mts = level == 0 ? (rows + 255) >> 8 : level == 1 ? (rows + 127) >> 7 : (rows + 63) >> 6;
     else c.mts = level == 0 ? (rows + 255) >> 8 : level == 1 ? (rows + 191) / 192 : level <= 3 ? (rows + 63) >> 6 : (rows + 31) >> 5;
     const int m = c.mts;
-    const bool few = rows <= 16 * m, some = rows <= 32 * m, half = rows <= 64 * m, more = rows <= 128 * m;
+    const int height = rows <= 16 * m ? 16 : rows <= 32 * m ? 32 : rows <= 64 * m ? 64 : rows <= 128 * m ? 128 : rows <= 160 * m ? 160 : rows <= 192 * m ? 192 : 256;
+    const int large = height == 128 ? 8 : height == 160 ? 9 : height == 192 ? 10 : 11;
     if (WIDE) {
-        c.tile = few ? 4 : some ? 5 : half ? 6 : 8;
+        c.tile = height == 16 ? 4 : height == 32 ? 5 : height == 64 ? 6 : large;
         c.width = 3;
     } else {
-        c.tile = level == 4 ? (few ? 0 : 1) : few ? 2 : some ? 3 : half ? (level == 3 ? 4 : 5) : level == 1 ? 6 : 8;
+        c.tile = level == 4      ? (height == 16 ? 0 : 1)
+                 : height == 16  ? 2
+                 : height == 32  ? 3
+                 : height == 64  ? (level == 3 ? 4 : 5)
+                 : level == 1    ? (height == 128 ? 6 : 7)
+                                 : large;
         c.width = c.tile < 2 ? 0 : c.tile < 5 ? 1 : c.tile < 8 ? 2 : 3;
     }
-    if (!more) c.tile = c.tile == 6 ? 7 : rows <= 192 * m ? 9 : 10;
+    c.cost = (64 + height) << c.width;
     if (rows == 0) c.tile = -1;
     return c;
 }
 
-// base[x] = tiles of the experts before x, of which this thread's two have n[0] and n[1].
-__device__ __forceinline__ void scan_tiles(const int (&n)[2], int X, int* base, int* part) {
+// base[x] = tiles of the experts before x; this thread's `each` experts have n[0] and n[1].
+__device__ __forceinline__ void scan_tiles(const int (&n)[2], int each, int X, int* base, int* part) {
     lds_barrier();  // the last kind's run is done with base
     const int v = n[0] + n[1], inc = wave_incl_scan(v);
     if (lane_id() == kWave - 1) part[wave_id()] = inc;
     lds_barrier();
     int before = inc - v;
-    for (int w = 0; w < wave_id(); ++w) before += part[w];
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w) before += w < wave_id() ? part[w] : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int x = 2 * threadIdx.x + i;
-        if (x <= X) base[x] = before;
+        const int x = each * threadIdx.x + i;
+        if (i < each && x <= X) base[x] = before;
         before += n[i];
     }
-    if (threadIdx.x == kThreads - 1) base[kMaxExperts] = before;
+    if (threadIdx.x == kThreads - 1 && X == each * kThreads) base[X] = before;
     lds_barrier();
 }
 
@@ -729,40 +660,55 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
     __shared__ __attribute__((aligned(16))) float epi[kEpiBytes / 4];
     __shared__ Experts E;
     __shared__ int part[kWaves];
-    __shared__ int sum[kLevels];
+    __shared__ unsigned long long sum[kLevels];
+    __shared__ int most[kLevels];
     __shared__ int present;
     const int X = P.rc * P.L, G = gridDim.x;
     // blocks of one XCD (the hardware deals blocks to the eight in turn) take neighbouring tiles
     const int per = G / 8, b = blockIdx.x;
     const int v = b < per * 8 ? b % 8 * per + b / 8 : b;
-    if (threadIdx.x < kLevels) sum[threadIdx.x] = 0;
+    if (threadIdx.x < kLevels) sum[threadIdx.x] = most[threadIdx.x] = 0;
     if (threadIdx.x == kLevels) present = 0;
     lds_barrier();
+    // (what follows runs once: it is kept short, as its code has to be fetched for it)
+    const int each = X > kThreads ? 2 : 1;  // experts a thread looks after
     int rows[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int x = 2 * threadIdx.x + i;
-        if (x < X) {
-            rows[i] = expert_rows(P, x, &E.first[x]);
-            E.rows[x] = rows[i];
-        }
+#pragma unroll 1
+    for (int i = 0; i < each; ++i) {
+        const int x = each * threadIdx.x + i;
+        if (x >= X) break;
+        const int n = expert_rows(P, x, &E.first[x]);
+        E.rows[x] = n;
+        rows[i & 1] = n;
     }
-    // (this part runs once: loops kept rolled, so that little code has to be fetched for it)
+    lds_barrier();
     constexpr int levels = WIDE ? 3 : kLevels;
     auto tiles_of = [&](const Choice& c) {
         const int w = c.width;
         return c.mts * (w == 0 ? P.ntn[0] : w == 1 ? P.ntn[1] : w == 2 ? P.ntn[2] : P.ntn[3]);
     };
-    if (rows[0] + rows[1]) {
 #pragma unroll 1
-        for (int l = 0; l < levels - 1; ++l) atomicAdd(&sum[l], tiles_of(choose<WIDE>(rows[0], l)) + tiles_of(choose<WIDE>(rows[1], l)));
+    for (int i = threadIdx.x; i < 4 * X; i += kThreads) {  // an expert at a level (but the last)
+        const int l = i & 3, n = E.rows[i >> 2];
+        if (n == 0 || l >= levels - 1) continue;
+        const Choice c = choose<WIDE>(n, l);
+        atomicAdd(&sum[l], (unsigned long long)tiles_of(c) * c.cost);
+        atomicMax(&most[l], c.cost);
     }
     lds_barrier();
     int level = 0;
 #pragma unroll 1
-    while (level < levels - 1 && sum[level] < kEnoughTiles) ++level;
-    const Choice mine[2] = {choose<WIDE>(rows[0], level), choose<WIDE>(rows[1], level)};
-    const int count[2] = {tiles_of(mine[0]), tiles_of(mine[1])};
+    while (level < levels - 1 && sum[level] < (unsigned long long)most[level] * (level == 3 ? kEnoughSmall : kEnough)) ++level;
+    level = uniform(level);
+    Choice mine[2];
+    int count[2] = {0, 0};
+    mine[1].tile = -1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (i == 1 && each == 1) break;
+        mine[i] = choose<WIDE>(rows[i], level);
+        count[i] = tiles_of(mine[i]);
+    }
     const int bits = (rows[0] ? 1 << mine[0].tile : 0) | (rows[1] ? 1 << mine[1].tile : 0);
     if (bits) atomicOr(&present, bits);
     lds_barrier();
@@ -772,12 +718,13 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
         typedef decltype(tile) T;
         if (!(all >> i & 1)) return;
         const int n[2] = {mine[0].tile == i ? count[0] : 0, mine[1].tile == i ? count[1] : 0};
-        scan_tiles(n, X, E.base, part);
+        scan_tiles(n, each, X, E.base, part);
         int w = v - done;
         w = w < 0 ? w + G : w;
         run_tiles<FP8, GATED, T>(P, ring, E, epi, X, w, G);
         done = (done + uniform(E.base[X])) % G;
     };
+    run(typename TileOf<KIND, 11>::type(), 11);
     run(typename TileOf<KIND, 10>::type(), 10);
     run(typename TileOf<KIND, 9>::type(), 9);
     run(typename TileOf<KIND, 8>::type(), 8);
