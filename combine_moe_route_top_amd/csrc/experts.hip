@@ -27,9 +27,9 @@ struct Product {
     int32_t* status;
     long B;       // rows per rank
     int KB, KS;   // bytes of a row; scales of a row (e4m3)
+    int quads;    // 1: rows of scales are whole 16-byte pieces; 0: they are not
     int C;
     int L, rb, rc;
-    int ntn[4];   // tiles side by side over the C columns, for tiles of 32, 64, 128 and 256 weight rows
 };
 
 constexpr int kStepBytes = 128;    // of every row, per step over K: 64 bf16 or 128 e4m3 values
@@ -255,7 +255,7 @@ struct Loader {
                 const float* of = j == 0   ? wscale + (long)block[0] * P.KS
                                   : j == 1 ? wscale + (long)block[1] * P.KS
                                            : rscale + (long)(r < last ? r : last) * P.KS;
-                if (P.KS % 4 == 0) {  // 16-byte rows of scales
+                if (P.quads) {
                     load_lds16(of + ks, to + w * 1024);
                 } else {
 #pragma unroll
@@ -407,9 +407,11 @@ template <bool FP8, bool GATED, class T>
 struct Wave {
     static constexpr int MT = T::MT, NT = T::NT;
     f32x4 acc[NT][MT];
-    float sr[MT], sw[2];  // e4m3: scales of the wave's rows and weight blocks
     i32x4 b[2][2];        // a part's rows and the next one's
+    float sr[2], sw[2];   // e4m3: their scales, and those of the wave's weight blocks
     int at_a, at_w, p0, p1;
+    const float* scales;  // e4m3: of the lane's row of part 0
+    int to_next;          // to part 1's
 
     __device__ __forceinline__ Wave() {
         const int lane = lane_id(), wave = uniform(wave_id());
@@ -437,18 +439,18 @@ struct Wave {
         const uint8_t* t = ring + slot * T::kRowSlot + at_a + j * T::WM * 16 * kStepBytes;
         b[j & 1][0] = *(const i32x4*)(t + p0);
         b[j & 1][1] = *(const i32x4*)(t + p1);
+        if constexpr (FP8) sr[j & 1] = scales[j * to_next];
     }
-    // The scales of stage k of a tile, in group `group` of the ring.
-    __device__ __forceinline__ void read_scales(const Product& P, const uint8_t* ring, int k, int group) {
+    // Finds the scales of stage k of a tile, in group `group` of the ring.
+    __device__ __forceinline__ void find_scales(const Product& P, const uint8_t* ring, int k, int group) {
         const int lane = lane_id(), wave = uniform(wave_id());
         const int wm = wave / T::WN % T::WM, wn = wave % T::WN, kp = wave / (T::WM * T::WN);
         // 16 bytes a row, or the four steps apart
-        const bool by_row = P.KS % 4 == 0;
-        const int one = by_row ? 4 : 1;
+        const int one = 1 + 3 * P.quads;
         const float* sc = (const float*)(ring + T::kScalesAt + group * T::kScaleSlot) +
-                          (k * T::KP + kp) % 4 * (by_row ? 1 : T::kScaleLoads * kWave);
-#pragma unroll
-        for (int j = 0; j < MT; ++j) sr[j] = sc[((j * T::WM + wm) * 16 + (lane & 15)) * one];
+                          (k * T::KP + kp) % 4 * (P.quads + (1 - P.quads) * T::kScaleLoads * kWave);
+        scales = sc + (wm * 16 + (lane & 15)) * one;
+        to_next = T::WM * 16 * one;
         sw[0] = sc[(T::BM + (GATED ? 0 : wn * NT * 16 / 128)) * one];
         sw[1] = GATED ? sc[(T::BM + 1) * one] : sw[0];
     }
@@ -462,7 +464,7 @@ struct Wave {
                 const i32x8 B = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
                 const f32x4 q =
                     __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-                const float s = sr[j] * sw[GATED ? (i & 1) : 0];
+                const float s = sr[j & 1] * sw[GATED ? (i & 1) : 0];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) acc[i][j][u] = __builtin_fmaf(q[u], s, acc[i][j][u]);
                 // here, and not after all products: the partial sums would need registers of their own
@@ -488,7 +490,8 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
     R.ring = lds_address(ring);
     R.X = X;
     R.G = G;
-    R.ntn = P.ntn[T::BN == 32 ? 0 : T::BN == 64 ? 1 : T::BN == 128 ? 2 : 3];
+    constexpr int kCols = GATED ? T::BN / 2 : T::BN;
+    R.ntn = (P.C + kCols - 1) / kCols;
     R.tiles = E.base[X];
     if (v >= R.tiles) return;
     R.stages = (P.KB + T::KP * kStepBytes - 1) / (T::KP * kStepBytes);
@@ -513,7 +516,7 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
     auto scales = [&] {
         if constexpr (FP8) {
             if (k * T::KP % 4 == 0) group = group == T::kScaleSlots - 1 ? 0 : group + 1;
-            W.read_scales(P, ring, k, group);
+            W.find_scales(P, ring, k, group);
         }
     };
     auto next = [&] {
@@ -683,9 +686,10 @@ __global__ __launch_bounds__(kThreads) void k_experts(Product P) {
     }
     lds_barrier();
     constexpr int levels = WIDE ? 3 : kLevels;
+    // a tile's columns are a power of two
     auto tiles_of = [&](const Choice& c) {
-        const int w = c.width;
-        return c.mts * (w == 0 ? P.ntn[0] : w == 1 ? P.ntn[1] : w == 2 ? P.ntn[2] : P.ntn[3]);
+        const int shift = c.width + (GATED ? 4 : 5);
+        return c.mts * ((P.C + (1 << shift) - 1) >> shift);
     };
 #pragma unroll 1
     for (int i = threadIdx.x; i < 4 * X; i += kThreads) {  // an expert at a level (but the last)
@@ -758,14 +762,11 @@ hipError_t launch_experts(const Dims& D, bool gated, int K, int C, const void* a
     P.B = D.B;
     P.KB = D.fp8 ? K : 2 * K;
     P.KS = K / 128;
+    P.quads = P.KS % 4 == 0 && ((uintptr_t)as | (uintptr_t)ws) % 16 == 0;
     P.C = C;
     P.L = D.L;
     P.rb = D.rb;
     P.rc = D.rc;
-    for (int i = 0; i < 4; ++i) {
-        const int cols = (gated ? 16 : 32) << i;
-        P.ntn[i] = (C + cols - 1) / cols;
-    }
     // one block a CU (each takes nearly all of its LDS); fewer if there cannot be as many tiles
     const long mts = (recv_rows_bound(D) + 15) / 16 + (long)D.rc * D.L;
     const int cols = D.fp8 && gated ? 128 : gated ? 16 : 32;

@@ -368,6 +368,26 @@ def test_weights_past_32_bits():
     ref.check_bf16("far weights", y[0].cpu(), *ref.product(x.view(torch.bfloat16).double(), W, False))
 
 
+def test_scales_at_any_4_byte_address():
+    """Scale arrays need only their own alignment: the same bits from arrays shifted by one float."""
+    s = Setup([[5, 70, 200]], 512, 256, True, "mlp", seed=8)
+    s.run()
+    torch.cuda.synchronize()
+    want = [t[:, : s.n_max].clone() for t in s.outputs()]
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, device="cuda")
+        flat[1:] = t.flatten()
+        return flat[1:].view(t.shape)
+
+    s.a_scale, s.w1s, s.w2s, s.hs = (shifted(t) for t in (s.a_scale, s.w1s, s.w2s, s.hs))
+    s.poison()
+    s.run()
+    s.check()
+    for now, was in zip(s.outputs(), want):
+        assert torch.equal(now[:, : s.n_max].contiguous().view(torch.uint8), was.view(torch.uint8))
+
+
 def test_shared_expert_is_one_group():
     """N = E = R = 1: the plain product of every token with one matrix."""
     for fp8, n in ((False, 77), (True, 333)):
