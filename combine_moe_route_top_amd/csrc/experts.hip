@@ -45,7 +45,7 @@ constexpr int kEpiBytes = 4 << 10;
 // and a value next to a border then falls to the other side; its tiles of up to this many rows, bound
 // by their weights' way from memory, multiply in bf16 instead (e4m3 values are bf16 values), which
 // costs 1% of a decode step's MLP.  Taller tiles keep the instruction, which is twice as fast.
-constexpr int kWidenRows = 64;
+constexpr int kWidenRows = 32;
 constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before the next one
 
 // A chunk of zeros: what lanes past the end of a row load in its last step.
