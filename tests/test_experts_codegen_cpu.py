@@ -33,7 +33,8 @@ def test_no_product_waits_for_the_loads_in_flight(tmp_path):
     assert len(kernels) == 4  # bf16 and e4m3, plain and gated
     for name, lines in kernels:
         products = [b for b in _blocks(lines) if any(l.startswith("v_mfma") for l in b)]
-        assert len(products) >= 8, name  # a loop for each kind of tile
+        # a loop for each kind of tile: 12, and 7 where a tile has whole blocks of 128 gated columns
+        assert len(products) >= (7 if "ILb1ELb1E" in name else 12), name
         waits = [l for b in products for l in b if "vmcnt" in l]
         assert not waits, (name, waits)
 
