@@ -5,6 +5,22 @@
 //             v[q][c] = sum_b as[q][b] ws[e][c/128][b] p_b[q][c]       e4m3: p_b the fp32 sum over the
 //                                                                      128 values k of block b
 //   gated     h = g / (1 + exp(-g)) * u,  g = v[q][c], u = v[q][I + c]
+//
+// One persistent block of 512 threads a CU reads the experts' row counts from the device, chooses a
+// tile for each expert by them (choose()), and walks its share of the tiles.  Rows and weights stream
+// through LDS rings by direct-to-LDS loads that run several stages ahead, across the ends of tiles; the
+// products are 16x16x32 (bf16) and 16x16x128 (e4m3) matrix instructions with fp32 accumulators.
+//
+// What bounds it (one MI355X; e4m3, K 7168 unless said):
+//  - few rows an expert: the weights' way from memory.  64 rows over 64 experts, 42 of them
+//    chosen, 4096 columns: 205 us, 6.0 TB/s of weights (plain reads of such row tiles reach 6.3-6.5,
+//    contiguous ones 7.1).
+//  - one token through 8 experts: 28 us for 134 MB of bf16 weights, of which 6 us are the start (row
+//    counts, choice, first loads) and 21 us the weights at 6.3 TB/s.
+//  - many rows: 256 x 256 tiles move 64 KB into LDS a step, and L2 gives a CU about 52 B/ns (13 TB/s in
+//    all), so a step takes at least 1.2 us; with its two barriers and 24 LDS reads a wave it takes
+//    1.9 (bf16, K 4096: 1.1 PFLOP/s) to 2.5 us (e4m3: 1.7 PFLOP/s; each product's scaling is a
+//    vector FMA for every accumulator, which alone leaves 3.5 of 4.2 PFLOP/s).
 #include "common.hpp"
 
 namespace moe {
@@ -46,7 +62,7 @@ constexpr int kEpiBytes = 4 << 10;
 // by their weights' way from memory, multiply in bf16 instead (e4m3 values are bf16 values), which
 // costs 1% of a decode step's MLP.  Taller tiles keep the instruction, which is twice as fast.
 constexpr int kWidenRows = 32;
-constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before the next one
+constexpr int kGroupTiles = 8;     // row tiles that share a weight tile before the next one (4: the same times)
 
 // A chunk of zeros: what lanes past the end of a row load in its last step.
 __device__ __attribute__((aligned(16))) const uint8_t kZeros[16] = {0};
@@ -594,7 +610,8 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
     };
     for (int t = v; t < R.tiles; t += G) {
         const Place p = place_of<T, GATED>(P, E, R, t);
-        for (k = 0; k < stages;) stage();
+        k = 0;
+        while (k < stages) stage();
         write_tile<FP8, GATED, T>(P, p, W.acc, epi);
         W.zero();
     }
@@ -604,6 +621,10 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
 // The tiles, from few rows and columns to many.  The gated product needs two 16-row parts of a tile's
 // weight rows in each wave (gate and up), and with e4m3 operands 256 of them in a tile: it quantises
 // blocks of 128 output columns.
+// Narrow tiles take two or four steps a stage: 256 and 512 bytes of a weight row in a row, which memory
+// gives at 6.3-6.5 TB/s, against 5.75-6.28 for 128.  Above 64 rows the rows' own way from L2 counts as
+// much as the weights', and wide tiles halve it.  160 rows: 32768 rows over 128 experts make two tiles of
+// about 130 rows for half of them; 1286 us with this tile, 1366 with 192 rows for them.
 constexpr int kLevels = 5;
 enum { kPlain, kGated, kWide };
 template <int KIND, int I> struct TileOf;
@@ -631,6 +652,9 @@ template <int KIND> struct TileOf<KIND, 11> { typedef Tile<256, 256, 2, 4, 1, 2,
 // the dearest of them (the last but one level: kEnoughSmall times).  Level 0 has the largest tiles,
 // further levels smaller ones.  At a level an expert's rows make as few row tiles as fit its most rows
 // each, and the tiles take the least height that holds their even share.
+// Measured (us at levels 0, 1, 2, 3, 4; the rule's choice in brackets): 1001 rows, 2048 columns, one expert
+// 119 71 [45] 52 -; 8 experts of 128 rows, 4096 columns 108 [82] 124 126 -; two ranks, 222 rows of K 1000
+// over 10 experts, 1288 columns 19 21 20 [17] 20; 8192 rows over 16 experts, K 2048 [133] 159 211 245 -.
 constexpr int kEnough = 192, kEnoughSmall = 64;
 struct Choice {
     int mts, tile;  // row tiles, and their kind (-1: no rows)
