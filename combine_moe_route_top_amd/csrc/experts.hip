@@ -401,7 +401,8 @@ __device__ __forceinline__ void write_tile(const Product& P, const Place& p, f32
                 float a = 0.0f;
 #pragma unroll
                 for (int q = 0; q < T::WN; ++q) a = fmaxf(a, epi[q * T::BM + (j * T::WM + wm) * 16 + r16]);
-                sc = a > 0.0f ? a / 448.0f : 1.0f;
+                sc = a / 448.0f;
+                if (sc == 0.0f) sc = 1.0f;  // also where a is below 2^-141: 0 / 0 would make NaN of its zeros
                 if (wn == 0 && lane < 16 && m < p.end) P.out_scale[(p.row0 + m) * (P.C / 128) + p.n0 / 128] = sc;
             }
 #pragma unroll

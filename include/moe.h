@@ -324,7 +324,8 @@ int moe_expert_gemm(const moe_shape* shape, int32_t K, int32_t C, const void* a,
  *   w            [E][2I][K], w_scale f32[E][2I/128][K/128] (e4m3): gate rows, then up rows
  *   h            bf16[N][B][I] (out), h rounded once; or e4m3 u8[N][B][I] (out)
  *   h_scale      f32[N][B][I/128] (out, e4m3), else NULL.  The e4m3 h is quantised from the fp32
- *                values by the rule of MOE_BF16_TO_FP8 (amax / 448 per 128 values, 1.0 for zeros);
+ *                values by the rule of MOE_BF16_TO_FP8 (amax / 448 per 128 values, 1.0 where that
+ *                rounds to zero, as it does below about 2^-141);
  *                a NaN keeps a NaN code */
 int moe_expert_gated(const moe_shape* shape, int32_t K, int32_t I, const void* a, const float* a_scale,
                      const void* w, const float* w_scale, const int32_t* expert_off, void* h,

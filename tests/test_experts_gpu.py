@@ -388,6 +388,24 @@ def test_scales_at_any_4_byte_address():
         assert torch.equal(now[:, : s.n_max].contiguous().view(torch.uint8), was.view(torch.uint8))
 
 
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("e,scale,code", [(-8, 1.0, 0.0), (-7, 2.0 ** -149, 256.0)])
+def test_gated_rows_next_to_zero(rows, e, scale, code):
+    """Gated e4m3 rows of which one half is zero and the other about the least fp32 values: 128 products
+    of ones, scaled, make gate and up 2^(-63 + e), so h is 2^(-127 + 2e), all exact.  For e = -8 its
+    448th, 2^-143 / 448, rounds to zero; for e = -7 it is 0.57 of the least fp32 value and rounds to it."""
+    s = Setup([[rows]], 128, 128, True, "gated")
+    s.a[:, :rows] = s.w1[:] = 0x38  # 1.0
+    s.w1[:, 128 + 64:] = 0          # up rows of the last 64 columns
+    s.a_scale[:, :rows] = 2.0 ** -70
+    s.w1s[:] = 2.0 ** e
+    s.run()
+    torch.cuda.synchronize()
+    assert bool((s.hs[0, :rows] == scale).all())
+    got = s.h[0, :rows].contiguous().view(torch.float8_e4m3fn).float()
+    assert bool((got[:, :64] == code).all()) and bool((got[:, 64:] == 0).all())
+
+
 def test_shared_expert_is_one_group():
     """N = E = R = 1: the plain product of every token with one matrix."""
     for fp8, n in ((False, 77), (True, 333)):
