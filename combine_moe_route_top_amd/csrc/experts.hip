@@ -624,7 +624,9 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
 // blocks of 128 output columns.
 // Narrow tiles take two or four steps a stage: 256 and 512 bytes of a weight row in a row, which memory
 // gives at 6.3-6.5 TB/s, against 5.75-6.28 for 128.  Above 64 rows the rows' own way from L2 counts as
-// much as the weights', and wide tiles halve it.  160 rows: 32768 rows over 128 experts make two tiles of
+// much as the weights', and wide tiles halve it.  From 128 rows on the weights' places are refilled before
+// the products: 8 experts of about 128 rows, K 7168, 4096 columns 72 us (192 x 128), 76 with a fifth stage of
+// weights instead; the 64 x 128 tile loses 9% by its second barrier.  160 rows: 32768 rows over 128 experts make two tiles of
 // about 130 rows for half of them; 1286 us with this tile, 1366 with 192 rows for them.
 constexpr int kLevels = 5;
 enum { kPlain, kGated, kWide };
@@ -639,8 +641,8 @@ template <> struct TileOf<kGated, 2> { typedef Tile<16, 64, 1, 2, 4, 3, 3> type;
 template <> struct TileOf<kGated, 3> { typedef Tile<32, 64, 2, 2, 2, 3, 7> type; };
 template <int KIND> struct TileOf<KIND, 4> { typedef Tile<64, 64, 2, 2, 2, 3, 5> type; };
 template <int KIND> struct TileOf<KIND, 5> { typedef Tile<64, 128, 2, 4, 1, 3, 7> type; };
-template <int KIND> struct TileOf<KIND, 6> { typedef Tile<128, 128, 2, 4, 1, 3, 5> type; };
-template <int KIND> struct TileOf<KIND, 7> { typedef Tile<192, 128, 2, 4, 1, 2, 5> type; };
+template <int KIND> struct TileOf<KIND, 6> { typedef Tile<128, 128, 2, 4, 1, 3, 3, kEarlyWeights> type; };
+template <int KIND> struct TileOf<KIND, 7> { typedef Tile<192, 128, 2, 4, 1, 2, 4, kEarlyWeights> type; };
 template <> struct TileOf<kWide, 4> { typedef Tile<16, 256, 1, 8, 1, 3, 4, kEarly> type; };
 template <> struct TileOf<kWide, 5> { typedef Tile<32, 256, 1, 8, 1, 2, 4, kEarly> type; };
 template <> struct TileOf<kWide, 6> { typedef Tile<64, 256, 1, 8, 1, 3, 3> type; };
@@ -654,7 +656,7 @@ template <int KIND> struct TileOf<KIND, 11> { typedef Tile<256, 256, 2, 4, 1, 2,
 // further levels smaller ones.  At a level an expert's rows make as few row tiles as fit its most rows
 // each, and the tiles take the least height that holds their even share.
 // Measured (us at levels 0, 1, 2, 3, 4; the rule's choice in brackets): 1001 rows, 2048 columns, one expert
-// 119 71 [45] 52 -; 8 experts of 128 rows, 4096 columns 108 [82] 124 126 -; two ranks, 222 rows of K 1000
+// 119 71 [45] 52 -; 8 experts of 128 rows, 4096 columns 108 [77] 124 126 -; two ranks, 222 rows of K 1000
 // over 10 experts, 1288 columns 19 21 20 [17] 20; 8192 rows over 16 experts, K 2048 [133] 159 211 245 -.
 constexpr int kEnough = 192, kEnoughSmall = 64;
 struct Choice {
