@@ -626,8 +626,8 @@ __device__ __forceinline__ void run_tiles(const Product& P, uint8_t* ring, const
 // gives at 6.3-6.5 TB/s, against 5.75-6.28 for 128.  Above 64 rows the rows' own way from L2 counts as
 // much as the weights', and wide tiles halve it.  From 128 rows on the weights' places are refilled before
 // the products: 8 experts of about 128 rows, K 7168, 4096 columns 72 us (192 x 128), 76 with a fifth stage of
-// weights instead; the 64 x 128 tile loses 9% by its second barrier.  160 rows: 32768 rows over 128 experts make two tiles of
-// about 130 rows for half of them; 1286 us with this tile, 1366 with 192 rows for them.
+// weights instead; the 64 x 128 tile loses 9% by its second barrier.  160 rows: 32768 rows over 128 experts make
+// two tiles of about 130 rows for half of them; 1286 us with this tile, 1366 with 192 rows for them.
 constexpr int kLevels = 5;
 enum { kPlain, kGated, kWide };
 template <int KIND, int I> struct TileOf;
